@@ -497,3 +497,8 @@ def matrix_stats(w: torch.Tensor, q: NVFP4Tensor | None = None, out: torch.Tenso
     if ret is not None:
         return ret
     return dict(zip(STAT_FIELDS, out[:7].cpu().tolist()))
+
+
+# MXFP4 entry points (include/mxfp4.h)
+from .mx import (MX_EXPORTED, MXFP4Tensor, mx_dequantize, mx_gemm, mx_gemm_workspace, mx_moe,  # noqa: E402
+                 mx_moe_workspace, mx_quantize, mx_workspace_size)

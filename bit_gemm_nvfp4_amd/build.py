@@ -26,7 +26,8 @@ FLAGS = [
     "-Wall", "-Wno-unused-result",
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
-SOURCES = ["api.hip", "quantize.hip", "dequantize.hip", "gemm.hip", "percentile.hip", "stats.hip", "lowrank.hip"]
+SOURCES = ["api.hip", "quantize.hip", "dequantize.hip", "gemm.hip", "percentile.hip", "stats.hip", "lowrank.hip",
+           "mx_api.hip", "mx_codec.hip", "mx_gemm.hip", "mx_moe.hip"]
 
 
 def _compile(src: str) -> str:

@@ -36,6 +36,8 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];
 std::atomic<int> g_dev_cus[kMaxDevices];
 
+}  // namespace
+
 // Check (once per device) that the current device is gfx950; returns its CU count or 0.
 int current_device_cus() {
     int dev = 0;
@@ -51,6 +53,8 @@ int current_device_cus() {
     }
     return st == 1 ? g_dev_cus[dev].load(std::memory_order_relaxed) : 0;
 }
+
+namespace {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

@@ -10,6 +10,9 @@
 
 namespace nvfp4 {
 
+// CU count of the current device if it is gfx950 (checked once per device), else 0.
+int current_device_cus();
+
 // Quantize workspace: a few words plus one 64-bit slot per workgroup of the single-pass kernel
 // (2040 slots: four workgroups per CU on parts with up to 510 CUs, two on larger ones).
 constexpr size_t kQuantizeWsBytes = 16384;

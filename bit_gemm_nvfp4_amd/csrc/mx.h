@@ -1,0 +1,112 @@
+// MXFP4 building blocks (E2M1 codes, one E8M0 scale per 32 elements of a row) shared by the mx_*.hip
+// kernels, and their host-side launchers.
+#pragma once
+
+#include "common.h"
+#include "mxfp4.h"
+
+namespace nvfp4 {
+
+constexpr int kMxBlock = 32;
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef u32x4 u32x4_u __attribute__((aligned(1)));  // 16 bytes at any address
+
+// E8M0 byte -> fp32 2^(b - 127): b = 0 is the subnormal 2^-127, b = 255 NaN.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
+    const uint32_t u = b == 0 ? 0x00400000u : b << 23;
+    return u2f(b == 255 ? 0x7FC00000u : u);
+}
+
+// The 32-bit operand of the scaled matrix instructions: four registers of 32 FP4 codes.
+__device__ __forceinline__ i32x8 fp4_operand(u32x4 c) {
+    return i32x8{(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};
+}
+
+// Rows of 16 (the operand of a 16-row matrix instruction) of an MXFP4 matrix, read straight from
+// global memory in groups of kGroup = 512 columns.  Lane l holds row l % 16; in chunk i (128 columns)
+// its 16 bytes are block l / 16, which is the operand layout of the 16 x 16 x 128 scaled instruction,
+// and a whole row chunk is 64 contiguous bytes.  The 16 scale bytes of a row's group come in one load,
+// byte l / 16 of word i being the lane's scale of chunk i.
+constexpr int kGroup = 512;
+constexpr int kGroupBlocks = kGroup / kMxBlock;
+constexpr int kGroupChunks = 4;
+
+struct MxGroup {
+    u32x4 c[kGroupChunks];
+    u32x4 s;
+};
+
+// codes and scales point at the lane's row.  nblk: blocks of the row from the start of the group on.
+__device__ __forceinline__ MxGroup load_mx_group(const uint8_t *codes, const uint8_t *scales, int64_t grp, int lg,
+                                                 int64_t nblk) {
+    MxGroup r;
+    const uint8_t *cp = codes + grp * (kGroup / 2) + lg * 16;
+    const uint8_t *sp = scales + grp * kGroupBlocks;
+    if (nblk >= kGroupBlocks) {
+#pragma unroll
+        for (int i = 0; i < kGroupChunks; i++) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
+        r.s = *reinterpret_cast<const u32x4_u *>(sp);
+    } else {  // the last, partial group: blocks past the row's end read as zero codes with scale 2^-127
+#pragma unroll
+        for (int i = 0; i < kGroupChunks; i++) {
+            r.c[i] = u32x4{0, 0, 0, 0};
+            if (i * 4 + lg < nblk) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
+        }
+        uint32_t s[4] = {0, 0, 0, 0};
+        for (int b = 0; b < (int)nblk; b++) {
+            const uint32_t v = sp[b];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (b / 4 == i) s[i] |= v << (8 * (b % 4));
+        }
+        r.s = u32x4{s[0], s[1], s[2], s[3]};
+    }
+    return r;
+}
+
+// Eight codes -> eight bf16 values e2m1 x 2^(b - 127), exact (the scaled conversion applies the exponent
+// of `scale`).
+__device__ __forceinline__ bf16x8 fp4_to_bf16x8(uint32_t w, float scale) {
+    bf16x2 p[4];
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+    return bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+}
+
+__device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Host side ---------------------------------------------------------------------------------------
+hipError_t launch_mx_quantize(const void *x, nvfp4_dtype dt, int64_t ld_x, const float *src_scale,
+                              const mxfp4_tensor *out, int32_t *flags, hipStream_t stream);
+hipError_t launch_mx_dequantize(const mxfp4_tensor *in, void *out, nvfp4_dtype out_dtype, int64_t ld_out,
+                                hipStream_t stream);
+
+// Workspace of mxfp4_gemm: the partial sums of the planned K slices, 0 when unsplit.
+size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus);
+hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+                          void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,
+                          int num_cus, hipStream_t stream);
+
+size_t mx_moe_ws_bytes(int64_t tokens, int64_t top_k, int64_t inter);
+struct MoeArgs {
+    const void *x;
+    int64_t tokens, ld_x;
+    const void *logits;
+    bool logits_bf16;
+    int64_t ld_logits, experts;
+    int top_k, renormalize;
+    const mxfp4_tensor *w_gate_up, *w_down;
+    void *y;
+    bool y_bf16;
+    int64_t ld_y;
+    int32_t *ids;
+    float *weights;
+};
+hipError_t launch_mx_moe(const MoeArgs &a, void *workspace, int num_cus, hipStream_t stream);
+
+}  // namespace nvfp4

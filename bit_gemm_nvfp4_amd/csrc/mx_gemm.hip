@@ -1,0 +1,547 @@
+// Products with MXFP4 weights for gfx950: C[M x N] = A . W^T, W [N x K] MXFP4, A MXFP4 or bf16.
+//
+// gfx950's scaled matrix instructions multiply FP4 (or FP8) operands with one E8M0 scale per 32
+// elements of K, which is MXFP4 as stored: codes and scale bytes go from memory to the matrix cores
+// without any expansion.
+//
+// k_mx_skinny (M <= 64): bound by streaming W.  A wave reads 16 W rows straight into registers in the
+//   operand layout (MxGroup), the waves of a workgroup split K and add their partial tiles in LDS in
+//   wave order.  MXFP4 activations take v_mfma_scale_f32_16x16x128; bf16 activations take
+//   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element).
+// k_mx_tile (M > 64): BM x BN output tile per workgroup, operands through LDS by direct-to-LDS loads,
+//   v_mfma_scale_f32_32x32x64 for MXFP4 activations, v_mfma_f32_32x32x16_bf16 for bf16 ones.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "internal.h"
+#include "mx.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kSkinnyMaxM = 64;
+
+template <class OT>
+__device__ __forceinline__ void store_out(OT *p, float v) {
+    *p = (OT)v;
+}
+
+// -------------------------------------------------------------------------------------------------
+// M <= 64
+// -------------------------------------------------------------------------------------------------
+// Activation fragments of chunk i of a group for 16 rows of A (lane: row l % 16, block l / 16).
+__device__ __forceinline__ void load_bf16_block(const __bf16 *row, int64_t blk, bool ok, bf16x8 *f) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (ok ? blk : 0) * kMxBlock);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const u32x4 v = p[j];
+        const u32x4 z = u32x4{0, 0, 0, 0};
+        f[j] = __builtin_bit_cast(bf16x8, ok ? v : z);
+    }
+}
+
+template <int CT, int RT, bool A_MX, class OT>
+__global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A, int64_t lda,
+                                                   const uint8_t *__restrict__ acodes,
+                                                   const uint8_t *__restrict__ ascales, int M,
+                                                   const uint8_t *__restrict__ wcodes,
+                                                   const uint8_t *__restrict__ wscales, int64_t N, int64_t K,
+                                                   OT *__restrict__ C, int64_t ldc) {
+    extern __shared__ float red[];  // [waves][RT][CT][256]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int r = lane & 15, lg = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    const int64_t kb = K / kMxBlock, kbytes = K / 2;
+    const uint8_t *wc[RT], *ws[RT];
+#pragma unroll
+    for (int i = 0; i < RT; i++) {  // rows past N repeat the last one; their results are not stored
+        const int64_t row = min(n0 + 16 * i + r, N - 1);
+        wc[i] = wcodes + row * kbytes;
+        ws[i] = wscales + row * kb;
+    }
+    int64_t arow[CT];
+#pragma unroll
+    for (int c = 0; c < CT; c++) arow[c] = min(c * 16 + r, M - 1);
+    f32x4 acc[RT][CT] = {};
+    const int64_t ngrp = (K + kGroup - 1) / kGroup;
+    for (int64_t g = wave; g < ngrp; g += waves) {
+        const int64_t nblk = kb - g * kGroupBlocks;
+        MxGroup w[RT];
+#pragma unroll
+        for (int i = 0; i < RT; i++) w[i] = load_mx_group(wc[i], ws[i], g, lg, nblk);
+        if constexpr (A_MX) {
+            MxGroup a[CT];
+#pragma unroll
+            for (int c = 0; c < CT; c++)
+                a[c] = load_mx_group(acodes + arow[c] * kbytes, ascales + arow[c] * kb, g, lg, nblk);
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; i++)
+#pragma unroll
+                for (int t = 0; t < RT; t++)
+#pragma unroll
+                    for (int c = 0; c < CT; c++)
+                        acc[t][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            fp4_operand(w[t].c[i]), fp4_operand(a[c].c[i]), acc[t][c], 4, 4, 0,
+                            (int)(w[t].s[i] >> (8 * lg)), 0, (int)(a[c].s[i] >> (8 * lg)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; i++) {
+                const bool ok = i * 4 + lg < nblk;
+                bf16x8 a[CT][4];
+#pragma unroll
+                for (int c = 0; c < CT; c++)
+                    load_bf16_block(A + arow[c] * lda, g * kGroupBlocks + i * 4 + lg, ok, a[c]);
+#pragma unroll
+                for (int t = 0; t < RT; t++) {
+                    const float s = e8m0_to_f32((w[t].s[i] >> (8 * lg)) & 255u);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const bf16x8 wf = fp4_to_bf16x8(w[t].c[i][j], s);
+#pragma unroll
+                        for (int c = 0; c < CT; c++) acc[t][c] = mfma_bf16(wf, a[c][j], acc[t][c]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; t++)
+#pragma unroll
+        for (int c = 0; c < CT; c++)
+            *reinterpret_cast<f32x4 *>(&red[((wave * RT + t) * CT + c) * 256 + lane * 4]) = acc[t][c];
+    __syncthreads();
+    // element (row nl of the tile, column m) sits in lane m % 16 + 16 (nl % 16 / 4), register nl % 4
+    for (int o = threadIdx.x; o < RT * CT * 256; o += blockDim.x) {
+        const int nl = o % (16 * RT), m = o / (16 * RT);
+        if (m >= M || n0 + nl >= N) continue;
+        const int at = ((nl / 16) * CT + m / 16) * 256 + (m % 16 + 16 * (nl % 16 / 4)) * 4 + nl % 4;
+        float s = 0.0f;
+        for (int v = 0; v < waves; v++) s += red[v * (RT * CT * 256) + at];
+        store_out(C + (int64_t)m * ldc + n0 + nl, s);
+    }
+}
+
+// -------------------------------------------------------------------------------------------------
+// M > 64
+// -------------------------------------------------------------------------------------------------
+// One LDS stage holds BK columns of the tile's rows as they are in memory: 128 bytes of an A row (256 MXFP4
+// or 64 bf16 elements) and BK / 2 bytes of a W row, in 16-byte pieces (an MXFP4 block, or 8 bf16 elements).
+// Pieces are stored XOR-swizzled by row so that the sixteen consecutive rows of one fragment read spread
+// over all banks.
+//
+// K order: within a step, lanes 0-31 of an operand hold blocks 0 .. KS - 1 and lanes 32-63 blocks KS .. 2 KS - 1,
+// KS = BK / 64, so the scale bytes a lane needs for a step are KS consecutive bytes of its row.
+//   MXFP4 A: instruction t takes block t of each half, the scale byte picked by its byte select.
+//   bf16 A: a lane expands its block of W with the scaled FP4 conversion (exact in bf16, four conversions
+//   per eight elements, used by all the wave's A rows) and v_mfma_f32_32x32x16_bf16 q takes elements
+//   8 q .. 8 q + 7 of each half's block.  An E4M3 pair per activation would keep W in four bits, but
+//   the FP8 matrix instructions align the products of eight elements to 13 bits of the largest, so the
+//   sum would lose what the pair carries.
+//
+// Scale bytes: 16 per row (512 columns, a window) in LDS, two windows; each thread loads its row's next
+// window into registers at the start of a window and writes it to LDS at the end.
+template <int BM_, int BN_, int WM_, int WN_, bool A_MX_, int NST_>
+struct MxTile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr bool A_MX = A_MX_;
+    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int BK = A_MX ? 256 : 64, KS = BK / 64;
+    static constexpr int A_ROWB = 128, W_ROWB = BK / 2;
+    static constexpr int W_PIECES = W_ROWB / 16;  // 8 or 2
+    static constexpr int W_OFF = BM * A_ROWB, STAGE = W_OFF + BN * W_ROWB;
+    static constexpr int NST = NST_;
+    static constexpr int WINDOW_STEPS = kGroup / BK;
+    static constexpr int SA_ROWS = A_MX ? BM : 0, SC_ROWS = SA_ROWS + BN, SC_OFF = NST * STAGE;
+    static constexpr int LDS_BYTES = SC_OFF + 2 * SC_ROWS * 16;
+    static constexpr int UNITS = STAGE / 1024, A_UNITS = W_OFF / 1024, UPW = UNITS / NW;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    static_assert(STAGE % 1024 == 0 && UNITS % NW == 0 && A_UNITS % NW == 0 && SC_ROWS <= NT, "tile shape");
+    static_assert(LDS_BYTES <= 160 * 1024 && NST >= 2 && NST <= WINDOW_STEPS + 1, "LDS stages");
+};
+
+// Position of 16-byte piece c of row `row` for rows of `pieces` pieces (8: 128 bytes, 2: 32 bytes): the
+// sixteen rows of a fragment read cover the 256 bytes of all banks once.
+template <int PIECES>
+__device__ __forceinline__ int swizzle(int row, int c) {
+    return PIECES == 8 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 3) & 1);
+}
+
+// Workgroup id -> tile: ids congruent mod 8 run on one XCD; each XCD gets a contiguous run of tiles in
+// bands of kBand tile rows, so that the tiles it works on at a time share A and W rows in its L2.
+constexpr int kBand = 4;
+__device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
+    const int total = tiles_m * tiles_n, per = (total + 7) / 8;
+    const int lin = (id % 8) * per + id / 8;
+    if (lin >= total || id / 8 >= per) return false;
+    const int band = lin / (kBand * tiles_n), in = lin % (kBand * tiles_n);
+    const int h = min(kBand, tiles_m - band * kBand);
+    tm = band * kBand + in % h;
+    tn = in / h;
+    return true;
+}
+
+__device__ __forceinline__ u32x4 load_scale_window(const uint8_t *row, int64_t window, int64_t kb) {
+    const int64_t nb = kb - window * kGroupBlocks;
+    const uint8_t *p = row + window * kGroupBlocks;
+    if (nb >= kGroupBlocks) return *reinterpret_cast<const u32x4_u *>(p);
+    uint32_t s[4] = {0, 0, 0, 0};
+    for (int b = 0; b < (int)nb; b++) {
+        const uint32_t v = p[b];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (b / 4 == i) s[i] |= v << (8 * (b % 4));
+    }
+    return u32x4{s[0], s[1], s[2], s[3]};
+}
+
+struct MxTileArgs {
+    const uint8_t *a;  // MXFP4 codes or bf16 rows
+    const uint8_t *ascales;
+    int64_t a_row_bytes, a_row_len;  // distance of two rows of A, and the bytes of a row that are read
+    const uint8_t *wcodes, *wscales;
+    int64_t M, N, K;
+    void *c;
+    int64_t ldc;
+    int tiles_m, tiles_n;
+    int slice_windows;  // windows of 512 columns per K slice (blockIdx.y)
+};
+
+// Matrix instructions t of a step (MXFP4 A): 64 columns.
+template <class T, int t>
+__device__ __forceinline__ void mx_kstep(const uint8_t *st, int arow, int wrow, int h, const int *sa, const int *sb,
+                                         f32x16 (&acc)[T::TM][T::TN]) {
+    i32x8 w[T::TN];
+#pragma unroll
+    for (int j = 0; j < T::TN; j++) {
+        const int row = wrow + 32 * j;
+        w[j] = fp4_operand(
+            *reinterpret_cast<const u32x4 *>(st + T::W_OFF + row * T::W_ROWB + swizzle<8>(row, 4 * h + t) * 16));
+    }
+#pragma unroll
+    for (int i = 0; i < T::TM; i++) {
+        const int row = arow + 32 * i;
+        const i32x8 a =
+            fp4_operand(*reinterpret_cast<const u32x4 *>(st + row * T::A_ROWB + swizzle<8>(row, 4 * h + t) * 16));
+#pragma unroll
+        for (int j = 0; j < T::TN; j++)
+            acc[i][j] =
+                __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, w[j], acc[i][j], 4, 4, t, sa[i], t, sb[j]);
+    }
+}
+
+// One step of 64 columns with bf16 A: the lane's W block of each column tile is expanded eight elements at
+// a time.
+template <class T>
+__device__ __forceinline__ void bf16_step(const uint8_t *st, int arow, int wrow, int h, const float *sb,
+                                          f32x16 (&acc)[T::TM][T::TN]) {
+    u32x4 w[T::TN];
+#pragma unroll
+    for (int j = 0; j < T::TN; j++) {
+        const int row = wrow + 32 * j;
+        w[j] = *reinterpret_cast<const u32x4 *>(st + T::W_OFF + row * T::W_ROWB + swizzle<2>(row, h) * 16);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        bf16x8 wf[T::TN];
+#pragma unroll
+        for (int j = 0; j < T::TN; j++) wf[j] = fp4_to_bf16x8(w[j][q], sb[j]);
+#pragma unroll
+        for (int i = 0; i < T::TM; i++) {
+            const int row = arow + 32 * i;
+            const bf16x8 a =
+                *reinterpret_cast<const bf16x8 *>(st + row * T::A_ROWB + swizzle<8>(row, 4 * h + q) * 16);
+#pragma unroll
+            for (int j = 0; j < T::TN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, wf[j], acc[i][j], 0, 0, 0);
+        }
+    }
+}
+
+template <class T, class OT, bool SPLIT>
+__global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
+    __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
+    int tm, tn;
+    if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5;
+    const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
+    const int64_t K = p.K, kb = K / kMxBlock;
+    const int64_t arb = p.a_row_bytes, wrb = K / 2;
+    const int alen = (int)p.a_row_len, wlen = (int)wrb;  // bytes of a row (K <= 2^23)
+    const int64_t mrows = min((int64_t)T::BM, p.M - m0), nrows = min((int64_t)T::BN, p.N - n0);
+    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.a + m0 * arb, (mrows - 1) * arb + alen);
+    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.wcodes + n0 * wrb, nrows * wrb);
+
+    const int64_t windows = (K + kGroup - 1) / kGroup;
+    const int64_t w0 = (int64_t)blockIdx.y * p.slice_windows, w1 = min(w0 + p.slice_windows, windows);
+    const int step0 = (int)(w0 * T::WINDOW_STEPS);
+    const int nsteps = (int)min((w1 - w0) * T::WINDOW_STEPS, (K + T::BK - 1) / T::BK - step0);
+
+    // this wave's direct-to-LDS loads: unit u fills 1 KiB of a stage (whole rows); units i < A_UNITS / NW
+    // are A's
+    uint32_t voff[T::UPW];
+    int pb[T::UPW];  // byte of the step's row part that this lane loads (bounds the last step)
+#pragma unroll
+    for (int i = 0; i < T::UPW; i++) {
+        const int u = wave + i * T::NW;
+        if (i < T::A_UNITS / T::NW) {
+            const int row = u * 8 + lane / 8;
+            pb[i] = swizzle<8>(row, lane % 8) * 16;
+            voff[i] = (uint32_t)(row * arb) + pb[i];
+            if (row >= mrows) voff[i] = kOffsetPastRange;
+        } else {
+            constexpr int PC = T::W_PIECES, RPU = 64 / PC;
+            const int row = (u - T::A_UNITS) * RPU + lane / PC;
+            pb[i] = swizzle<PC>(row, lane % PC) * 16;
+            voff[i] = (uint32_t)(row * wrb) + pb[i];
+        }
+    }
+    auto load_stage = [&](int s) {  // step s of the slice
+        uint8_t *dst = lds + (s % T::NST) * T::STAGE + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < T::UPW; i++) {
+            const bool isa = i < T::A_UNITS / T::NW;
+            const int soff = (step0 + s) * (isa ? T::A_ROWB : T::W_ROWB);
+            // past the end of the row the load returns zeros
+            const uint32_t v = soff + pb[i] < (isa ? alen : wlen) ? voff[i] : kOffsetPastRange;
+            load_to_lds16(isa ? ra : rw, dst + i * (T::NW * 1024), v, soff);
+        }
+    };
+    // scale rows: thread tid < SC_ROWS serves row tid of [A rows (MXFP4 A), W rows]
+    const uint8_t *srow = nullptr;
+    if (tid < T::SA_ROWS) {
+        if (tid < mrows) srow = p.ascales + (m0 + tid) * kb;
+    } else if (tid < T::SC_ROWS) {
+        if (tid - T::SA_ROWS < nrows) srow = p.wscales + (n0 + tid - T::SA_ROWS) * kb;
+    }
+    auto load_scales = [&](int64_t w) { return srow ? load_scale_window(srow, w, kb) : u32x4{0, 0, 0, 0}; };
+    auto put_scales = [&](int64_t w, u32x4 v) {
+        if (tid < T::SC_ROWS)
+            *reinterpret_cast<u32x4 *>(lds + T::SC_OFF + (int)(w & 1) * (T::SC_ROWS * 16) + tid * 16) = v;
+    };
+
+    f32x16 acc[T::TM][T::TN] = {};
+    const int arow = (wave / T::WN) * T::WTM + (lane & 31), wrow = (wave % T::WN) * T::WTN + (lane & 31);
+    u32x4 snext = u32x4{0, 0, 0, 0};
+    if (nsteps > 0) put_scales(w0, load_scales(w0));
+#pragma unroll
+    for (int s = 0; s < T::NST - 1; s++)
+        if (s < nsteps) load_stage(s);
+    for (int s = 0; s < nsteps; s++) {
+        const int64_t win = w0 + s / T::WINDOW_STEPS;
+        const int in = s % T::WINDOW_STEPS;
+        // stage s has landed when at most the loads of the NST - 2 later stages are outstanding: every wave
+        // waits for its own loads, then all meet.  The stage of step s - 1 and the other scale window are
+        // then no longer read by anyone.
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + T::NST - 2 < nsteps) __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 2) * T::UPW, 0));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + T::NST - 1 < nsteps) load_stage(s + T::NST - 1);
+        if (in == 0 && win + 1 < w1) snext = load_scales(win + 1);
+        const uint8_t *st = lds + (s % T::NST) * T::STAGE;
+        const uint8_t *sc = lds + T::SC_OFF + (int)(win & 1) * (T::SC_ROWS * 16);
+        if constexpr (T::A_MX) {
+            int sa[T::TM], sb[T::TN];
+#pragma unroll
+            for (int i = 0; i < T::TM; i++)
+                sa[i] = *reinterpret_cast<const int *>(sc + (arow + 32 * i) * 16 + in * 8 + h * 4);
+#pragma unroll
+            for (int j = 0; j < T::TN; j++)
+                sb[j] = *reinterpret_cast<const int *>(sc + (T::SA_ROWS + wrow + 32 * j) * 16 + in * 8 + h * 4);
+            mx_kstep<T, 0>(st, arow, wrow, h, sa, sb, acc);
+            mx_kstep<T, 1>(st, arow, wrow, h, sa, sb, acc);
+            mx_kstep<T, 2>(st, arow, wrow, h, sa, sb, acc);
+            mx_kstep<T, 3>(st, arow, wrow, h, sa, sb, acc);
+        } else {
+            float sb[T::TN];
+#pragma unroll
+            for (int j = 0; j < T::TN; j++) sb[j] = e8m0_to_f32(sc[(wrow + 32 * j) * 16 + in * 2 + h]);
+            bf16_step<T>(st, arow, wrow, h, sb, acc);
+        }
+        if (in == T::WINDOW_STEPS - 1 && win + 1 < w1) put_scales(win + 1, snext);
+    }
+
+    OT *c = reinterpret_cast<OT *>(p.c);
+    if constexpr (SPLIT) c += (int64_t)blockIdx.y * p.M * p.N;
+#pragma unroll
+    for (int i = 0; i < T::TM; i++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            const int64_t m = m0 + (wave / T::WN) * T::WTM + 32 * i + 8 * (e / 4) + 4 * h + e % 4;
+            if (m >= p.M) continue;
+#pragma unroll
+            for (int j = 0; j < T::TN; j++) {
+                const int64_t n = n0 + wrow + 32 * j;
+                if (n < p.N) store_out(c + m * (SPLIT ? p.N : p.ldc) + n, acc[i][j][e]);
+            }
+        }
+}
+
+// C = the sum of the K slices' partial planes, in slice order.
+template <class OT>
+__global__ __launch_bounds__(256) void k_mx_reduce(const float *__restrict__ P, int splits, int64_t M, int64_t N,
+                                                   OT *__restrict__ C, int64_t ldc) {
+    const int64_t n = M * N;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        float s = P[i];
+        for (int k = 1; k < splits; k++) s += P[k * n + i];
+        const int64_t m = i / N;
+        store_out(C + m * ldc + (i - m * N), s);
+    }
+}
+
+template <class OT>
+__global__ __launch_bounds__(256) void k_mx_zero(OT *C, int64_t M, int64_t N, int64_t ldc) {
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * blockDim.x)
+        C[(i / N) * ldc + i % N] = (OT)0.0f;
+}
+
+// -------------------------------------------------------------------------------------------------
+// launches
+// -------------------------------------------------------------------------------------------------
+struct MxPlan {
+    int cfg;            // 0: 256-row tiles, 1: 128-row tiles
+    int splits;         // K slices
+    int slice_windows;  // windows of 512 columns per slice
+};
+
+constexpr int kMaxSplits = 8;
+
+MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
+    const int64_t windows = (K + kGroup - 1) / kGroup;
+    MxPlan best{0, 1, (int)windows};
+    double cost = 1e30;
+    for (int cfg = 0; cfg < 2; cfg++) {
+        const int bm = cfg == 0 ? 256 : 128, bn = bm;
+        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplits, windows); s++) {
+            const int64_t per = (windows + s - 1) / s, used = (windows + per - 1) / per;
+            if (used != s) continue;
+            const double rounds = (double)((tiles * s + num_cus - 1) / num_cus);
+            double us = rounds * (per * bm * bn * (cfg == 0 ? 1.0 : 1.4) * 3.5e-5 * (a_mx ? 1.0 : 4.0) + 3.0);
+            if (s > 1) us += 4.0 + (double)M * N * 4 * (s + 1) / 4.0e6;
+            if (us < cost) {
+                cost = us;
+                best = MxPlan{cfg, (int)s, (int)per};
+            }
+        }
+    }
+    return best;
+}
+
+template <class T, class OT>
+void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) {
+    p.tiles_m = (int)((p.M + T::BM - 1) / T::BM);
+    p.tiles_n = (int)((p.N + T::BN - 1) / T::BN);
+    const int per = (p.tiles_m * p.tiles_n + 7) / 8;
+    const dim3 grid(per * 8, splits);
+    if (splits == 1) {
+        hipLaunchKernelGGL((k_mx_tile<T, OT, false>), grid, dim3(T::NT), 0, stream, p);
+        return;
+    }
+    OT *c = reinterpret_cast<OT *>(p.c);
+    p.c = partial;
+    hipLaunchKernelGGL((k_mx_tile<T, float, true>), grid, dim3(T::NT), 0, stream, p);
+    const int64_t blocks = std::min<int64_t>((p.M * p.N + 255) / 256, 8192);
+    hipLaunchKernelGGL(k_mx_reduce<OT>, dim3((unsigned)blocks), dim3(256), 0, stream,
+                       reinterpret_cast<const float *>(partial), splits, p.M, p.N, c, p.ldc);
+}
+
+template <class OT>
+void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
+                  int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, hipStream_t stream) {
+    MxTileArgs p{};
+    p.M = M;
+    p.N = w->rows;
+    p.K = w->cols;
+    p.wcodes = w->codes;
+    p.wscales = w->scales;
+    p.c = c;
+    p.ldc = ldc;
+    const bool a_mx = a_q != nullptr;
+    p.a = a_mx ? a_q->codes : reinterpret_cast<const uint8_t *>(a_bf16);
+    p.ascales = a_mx ? a_q->scales : nullptr;
+    p.a_row_bytes = a_mx ? p.K / 2 : lda * 2;
+    p.a_row_len = a_mx ? p.K / 2 : p.K * 2;
+    MxPlan plan = plan_mx(M, p.N, p.K, a_mx, num_cus);
+    if (plan.splits > 1 && (!workspace || workspace_bytes < (size_t)plan.splits * M * p.N * 4)) {
+        plan.splits = 1;
+        plan.slice_windows = (int)((p.K + kGroup - 1) / kGroup);
+    }
+    p.slice_windows = plan.slice_windows;
+    if (a_mx) {
+        if (plan.cfg == 0) launch_tile_t<MxTile<256, 256, 2, 4, true, 2>, OT>(p, plan.splits, workspace, stream);
+        else launch_tile_t<MxTile<128, 128, 2, 2, true, 2>, OT>(p, plan.splits, workspace, stream);
+    } else {
+        if (plan.cfg == 0) launch_tile_t<MxTile<256, 256, 2, 4, false, 3>, OT>(p, plan.splits, workspace, stream);
+        else launch_tile_t<MxTile<128, 128, 2, 2, false, 3>, OT>(p, plan.splits, workspace, stream);
+    }
+}
+
+template <int CT, int RT, bool A_MX, class OT>
+void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
+                     int64_t ldc, int num_cus, hipStream_t stream) {
+    const int64_t N = w->rows, K = w->cols;
+    const int64_t wgs = (N + 16 * RT - 1) / (16 * RT), groups = (K + kGroup - 1) / kGroup;
+    // enough waves to keep about 12 per CU streaming, no more than there are groups to share out
+    int waves = 4;
+    if (wgs * waves < 12 * (int64_t)num_cus) waves = 8;
+    while (waves > 1 && waves / 2 >= groups) waves /= 2;
+    const size_t lds = (size_t)waves * RT * CT * 1024;
+    hipLaunchKernelGGL((k_mx_skinny<CT, RT, A_MX, OT>), dim3((unsigned)wgs), dim3(64 * waves), lds, stream,
+                       reinterpret_cast<const __bf16 *>(a_bf16), lda, A_MX ? a_q->codes : nullptr,
+                       A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, N, K, c, ldc);
+}
+
+template <class OT>
+void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
+                   int64_t ldc, int num_cus, hipStream_t stream) {
+    const int ct = (int)((M + 15) / 16);
+#define MX_SKINNY(CT)                                                                                        \
+    (a_q ? launch_skinny_t<CT, 1, true, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream)                 \
+         : launch_skinny_t<CT, 1, false, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream))
+    if (ct == 1) MX_SKINNY(1);
+    else if (ct == 2) MX_SKINNY(2);
+    else MX_SKINNY(4);
+#undef MX_SKINNY
+}
+
+template <class OT>
+hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+                            OT *c, int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus,
+                            hipStream_t stream) {
+    if (w->cols == 0) {
+        const int64_t blocks = std::min<int64_t>((M * w->rows + 255) / 256, 4096);
+        hipLaunchKernelGGL(k_mx_zero<OT>, dim3((unsigned)blocks), dim3(256), 0, stream, c, M, w->rows, ldc);
+    } else if (M <= kSkinnyMaxM) {
+        launch_skinny(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+    } else {
+        launch_tiled(a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
+    if (M <= kSkinnyMaxM || N <= 0 || K <= 0) return 0;
+    const MxPlan plan = plan_mx(M, N, K, a_mx, num_cus);
+    return plan.splits > 1 ? (size_t)plan.splits * M * N * 4 : 0;
+}
+
+hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+                          void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,
+                          int num_cus, hipStream_t stream) {
+    if (c_dtype == NVFP4_F32)
+        return launch_mx_gemm_t(a_bf16, a_q, M, lda, w, reinterpret_cast<float *>(c), ldc, workspace, workspace_bytes,
+                                num_cus, stream);
+    return launch_mx_gemm_t(a_bf16, a_q, M, lda, w, reinterpret_cast<__bf16 *>(c), ldc, workspace, workspace_bytes,
+                            num_cus, stream);
+}
+
+}  // namespace nvfp4
