@@ -158,8 +158,9 @@ struct MxTile {
     static constexpr int LDS_BYTES = SC_OFF + 2 * SC_ROWS * 16;
     static constexpr int UNITS = STAGE / 1024, A_UNITS = W_OFF / 1024, UPW = UNITS / NW;
     static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    static_assert(NW % 2 == 0, "the units of a wave share a swizzle");
     static_assert(STAGE % 1024 == 0 && UNITS % NW == 0 && A_UNITS % NW == 0 && SC_ROWS <= NT, "tile shape");
-    static_assert(LDS_BYTES <= 160 * 1024 && NST >= 2 && NST <= WINDOW_STEPS + 1, "LDS stages");
+    static_assert(LDS_BYTES <= 160 * 1024 && NST >= 2, "LDS stages");
 };
 
 // Position of 16-byte piece c of row `row` for rows of `pieces` pieces (8: 128 bytes, 2: 32 bytes): the
@@ -178,23 +179,32 @@ __device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int &t
     if (lin >= total || id / 8 >= per) return false;
     const int band = lin / (kBand * tiles_n), in = lin % (kBand * tiles_n);
     const int h = min(kBand, tiles_m - band * kBand);
-    tm = band * kBand + in % h;
-    tn = in / h;
+    tm = __builtin_amdgcn_readfirstlane(band * kBand + in % h);
+    tn = __builtin_amdgcn_readfirstlane(in / h);
     return true;
 }
 
-__device__ __forceinline__ u32x4 load_scale_window(const uint8_t *row, int64_t window, int64_t kb) {
-    const int64_t nb = kb - window * kGroupBlocks;
+__device__ __forceinline__ u32x4 load_scale_window(const uint8_t *row, int window, int kb) {
+    const int nb = kb - window * kGroupBlocks;
     const uint8_t *p = row + window * kGroupBlocks;
     if (nb >= kGroupBlocks) return *reinterpret_cast<const u32x4_u *>(p);
     uint32_t s[4] = {0, 0, 0, 0};
-    for (int b = 0; b < (int)nb; b++) {
+    for (int b = 0; b < nb; b++) {
         const uint32_t v = p[b];
 #pragma unroll
         for (int i = 0; i < 4; i++)
             if (b / 4 == i) s[i] |= v << (8 * (b % 4));
     }
     return u32x4{s[0], s[1], s[2], s[3]};
+}
+
+// buffer_rsrc with its words forced into scalar registers: a base formed by vector 64-bit arithmetic, though
+// the same in every lane, would have each load wrapped in a loop over the lanes' values.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const uint8_t *base, uint32_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return buffer_rsrc(reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo),
+                       (uint32_t)__builtin_amdgcn_readfirstlane(bytes));
 }
 
 struct MxTileArgs {
@@ -209,57 +219,44 @@ struct MxTileArgs {
     int slice_windows;  // windows of 512 columns per K slice (blockIdx.y)
 };
 
-// Matrix instructions t of a step (MXFP4 A): 64 columns.
+// Operands of one quarter of a step, and its matrix instructions.
+template <class T>
+struct MxFrags {
+    u32x4 a[T::TM], w[T::A_MX ? T::TN : 1];
+};
+
+// Quarter t: the 64 columns of blocks t and 4 + t (MXFP4 A).
 template <class T, int t>
-__device__ __forceinline__ void mx_kstep(const uint8_t *st, int arow, int wrow, int h, const int *sa, const int *sb,
-                                         f32x16 (&acc)[T::TM][T::TN]) {
-    i32x8 w[T::TN];
+__device__ __forceinline__ void mx_quarter(const MxFrags<T> &f, const int (&sa)[T::TM], const int (&sb)[T::TN],
+                                           f32x16 (&acc)[T::TM][T::TN]) {
 #pragma unroll
-    for (int j = 0; j < T::TN; j++) {
-        const int row = wrow + 32 * j;
-        w[j] = fp4_operand(
-            *reinterpret_cast<const u32x4 *>(st + T::W_OFF + row * T::W_ROWB + swizzle<8>(row, 4 * h + t) * 16));
-    }
-#pragma unroll
-    for (int i = 0; i < T::TM; i++) {
-        const int row = arow + 32 * i;
-        const i32x8 a =
-            fp4_operand(*reinterpret_cast<const u32x4 *>(st + row * T::A_ROWB + swizzle<8>(row, 4 * h + t) * 16));
+    for (int i = 0; i < T::TM; i++)
 #pragma unroll
         for (int j = 0; j < T::TN; j++)
-            acc[i][j] =
-                __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, w[j], acc[i][j], 4, 4, t, sa[i], t, sb[j]);
-    }
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f.a[i]), fp4_operand(f.w[j]),
+                                                                       acc[i][j], 4, 4, t, sa[i], t, sb[j]);
 }
 
-// One step of 64 columns with bf16 A: the lane's W block of each column tile is expanded eight elements at
-// a time.
+// Quarter q: elements 8 q .. 8 q + 7 of the two blocks of a step, W expanded to bf16 (bf16 A).
 template <class T>
-__device__ __forceinline__ void bf16_step(const uint8_t *st, int arow, int wrow, int h, const float *sb,
-                                          f32x16 (&acc)[T::TM][T::TN]) {
-    u32x4 w[T::TN];
+__device__ __forceinline__ void bf16_quarter(const MxFrags<T> &f, int q, const u32x4 (&w)[T::TN],
+                                             const float (&sb)[T::TN], f32x16 (&acc)[T::TM][T::TN]) {
+    bf16x8 wf[T::TN];
 #pragma unroll
-    for (int j = 0; j < T::TN; j++) {
-        const int row = wrow + 32 * j;
-        w[j] = *reinterpret_cast<const u32x4 *>(st + T::W_OFF + row * T::W_ROWB + swizzle<2>(row, h) * 16);
-    }
+    for (int j = 0; j < T::TN; j++) wf[j] = fp4_to_bf16x8(w[j][q], sb[j]);
 #pragma unroll
-    for (int q = 0; q < 4; q++) {
-        bf16x8 wf[T::TN];
+    for (int i = 0; i < T::TM; i++)
 #pragma unroll
-        for (int j = 0; j < T::TN; j++) wf[j] = fp4_to_bf16x8(w[j][q], sb[j]);
-#pragma unroll
-        for (int i = 0; i < T::TM; i++) {
-            const int row = arow + 32 * i;
-            const bf16x8 a =
-                *reinterpret_cast<const bf16x8 *>(st + row * T::A_ROWB + swizzle<8>(row, 4 * h + q) * 16);
-#pragma unroll
-            for (int j = 0; j < T::TN; j++)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, wf[j], acc[i][j], 0, 0, 0);
-        }
-    }
+        for (int j = 0; j < T::TN; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f.a[i]), wf[j], acc[i][j],
+                                                                0, 0, 0);
 }
 
+// The main loop runs in quarters of a step with the operands of the next quarter read from LDS while the
+// matrix instructions of this one issue.  The step's one barrier stands before its last quarter, whose
+// operands are then in registers: behind it stage s + 1 is complete in LDS, so the first operands of
+// step s + 1 are read under the last quarter's instructions, and stage s may be overwritten, so the
+// loads of step s + NST are issued.
 template <class T, class OT, bool SPLIT>
 __global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
@@ -268,103 +265,146 @@ __global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5;
     const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
-    const int64_t K = p.K, kb = K / kMxBlock;
-    const int64_t arb = p.a_row_bytes, wrb = K / 2;
-    const int alen = (int)p.a_row_len, wlen = (int)wrb;  // bytes of a row (K <= 2^23)
-    const int64_t mrows = min((int64_t)T::BM, p.M - m0), nrows = min((int64_t)T::BN, p.N - n0);
-    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(p.a + m0 * arb, (mrows - 1) * arb + alen);
-    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(p.wcodes + n0 * wrb, nrows * wrb);
+    const int K = (int)p.K, kb = K / kMxBlock;
+    const int arb = (int)p.a_row_bytes, wrb = K / 2;  // below 2^23
+    const int alen = (int)p.a_row_len, wlen = wrb;    // bytes of a row
+    const int mrows = min(T::BM, (int)p.M - tm * T::BM), nrows = min(T::BN, (int)p.N - tn * T::BN);
+    const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(p.a + m0 * arb, (uint32_t)((mrows - 1) * arb + alen));
+    const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(p.wcodes + n0 * wrb, (uint32_t)(nrows * wrb));
 
-    const int64_t windows = (K + kGroup - 1) / kGroup;
-    const int64_t w0 = (int64_t)blockIdx.y * p.slice_windows, w1 = min(w0 + p.slice_windows, windows);
-    const int step0 = (int)(w0 * T::WINDOW_STEPS);
-    const int nsteps = (int)min((w1 - w0) * T::WINDOW_STEPS, (K + T::BK - 1) / T::BK - step0);
+    const int windows = (K + kGroup - 1) / kGroup;
+    const int w0 = (int)blockIdx.y * p.slice_windows, w1 = min(w0 + p.slice_windows, windows);
+    const int step0 = w0 * T::WINDOW_STEPS;
+    const int nsteps = min((w1 - w0) * T::WINDOW_STEPS, (K + T::BK - 1) / T::BK - step0);
 
-    // this wave's direct-to-LDS loads: unit u fills 1 KiB of a stage (whole rows); units i < A_UNITS / NW
-    // are A's
-    uint32_t voff[T::UPW];
-    int pb[T::UPW];  // byte of the step's row part that this lane loads (bounds the last step)
-#pragma unroll
-    for (int i = 0; i < T::UPW; i++) {
-        const int u = wave + i * T::NW;
-        if (i < T::A_UNITS / T::NW) {
-            const int row = u * 8 + lane / 8;
-            pb[i] = swizzle<8>(row, lane % 8) * 16;
-            voff[i] = (uint32_t)(row * arb) + pb[i];
-            if (row >= mrows) voff[i] = kOffsetPastRange;
-        } else {
-            constexpr int PC = T::W_PIECES, RPU = 64 / PC;
-            const int row = (u - T::A_UNITS) * RPU + lane / PC;
-            pb[i] = swizzle<PC>(row, lane % PC) * 16;
-            voff[i] = (uint32_t)(row * wrb) + pb[i];
-        }
-    }
+    // Direct-to-LDS loads: unit u = wave + NW i fills 1 KiB of a stage (8 rows of 128 bytes, or 32 of 32).
+    // The rows of a wave's units differ by multiples of 32, so the lane part of the offset and the
+    // swizzle are the same for all of them and the rest is a scalar offset.  Rows past M or N lie past
+    // the buffer's range and load zeros; so do pieces past the end of a row (kOffsetPastRange).
+    constexpr int A_PER = T::A_UNITS / T::NW, RPU = 64 / T::W_PIECES;
+    const int ar = wave * 8 + lane / 8, wr = wave * RPU + lane / T::W_PIECES;
+    const int apb = swizzle<8>(ar, lane % 8) * 16, wpb = swizzle<T::W_PIECES>(wr, lane % T::W_PIECES) * 16;
+    const uint32_t avo = (uint32_t)(ar * arb + apb), wvo = (uint32_t)(wr * wrb + wpb);
     auto load_stage = [&](int s) {  // step s of the slice
         uint8_t *dst = lds + (s % T::NST) * T::STAGE + wave * 1024;
+        const int ao = (step0 + s) * T::A_ROWB, wo = (step0 + s) * T::W_ROWB;
+        const uint32_t av = ao + apb < alen ? avo : kOffsetPastRange;
+        const uint32_t wv = wo + wpb < wlen ? wvo : kOffsetPastRange;
 #pragma unroll
         for (int i = 0; i < T::UPW; i++) {
-            const bool isa = i < T::A_UNITS / T::NW;
-            const int soff = (step0 + s) * (isa ? T::A_ROWB : T::W_ROWB);
-            // past the end of the row the load returns zeros
-            const uint32_t v = soff + pb[i] < (isa ? alen : wlen) ? voff[i] : kOffsetPastRange;
-            load_to_lds16(isa ? ra : rw, dst + i * (T::NW * 1024), v, soff);
+            if (i < A_PER) load_to_lds16(ra, dst + i * (T::NW * 1024), av, ao + i * (T::NW * 8) * arb);
+            else load_to_lds16(rw, dst + i * (T::NW * 1024), wv, wo + (i - A_PER) * (T::NW * RPU) * wrb);
         }
     };
     // scale rows: thread tid < SC_ROWS serves row tid of [A rows (MXFP4 A), W rows]
     const uint8_t *srow = nullptr;
     if (tid < T::SA_ROWS) {
-        if (tid < mrows) srow = p.ascales + (m0 + tid) * kb;
+        if (tid < mrows) srow = p.ascales + (m0 + tid) * (int64_t)kb;
     } else if (tid < T::SC_ROWS) {
-        if (tid - T::SA_ROWS < nrows) srow = p.wscales + (n0 + tid - T::SA_ROWS) * kb;
+        if (tid - T::SA_ROWS < nrows) srow = p.wscales + (n0 + tid - T::SA_ROWS) * (int64_t)kb;
     }
-    auto load_scales = [&](int64_t w) { return srow ? load_scale_window(srow, w, kb) : u32x4{0, 0, 0, 0}; };
-    auto put_scales = [&](int64_t w, u32x4 v) {
+    auto load_scales = [&](int w) { return srow ? load_scale_window(srow, w, kb) : u32x4{0, 0, 0, 0}; };
+    auto put_scales = [&](int w, u32x4 v) {
         if (tid < T::SC_ROWS)
-            *reinterpret_cast<u32x4 *>(lds + T::SC_OFF + (int)(w & 1) * (T::SC_ROWS * 16) + tid * 16) = v;
+            *reinterpret_cast<u32x4 *>(lds + T::SC_OFF + (w & 1) * (T::SC_ROWS * 16) + tid * 16) = v;
     };
 
-    f32x16 acc[T::TM][T::TN] = {};
     const int arow = (wave / T::WN) * T::WTM + (lane & 31), wrow = (wave % T::WN) * T::WTN + (lane & 31);
-    u32x4 snext = u32x4{0, 0, 0, 0};
-    if (nsteps > 0) put_scales(w0, load_scales(w0));
-#pragma unroll
-    for (int s = 0; s < T::NST - 1; s++)
-        if (s < nsteps) load_stage(s);
-    for (int s = 0; s < nsteps; s++) {
-        const int64_t win = w0 + s / T::WINDOW_STEPS;
-        const int in = s % T::WINDOW_STEPS;
-        // stage s has landed when at most the loads of the NST - 2 later stages are outstanding: every wave
-        // waits for its own loads, then all meet.  The stage of step s - 1 and the other scale window are
-        // then no longer read by anyone.
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + T::NST - 2 < nsteps) __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 2) * T::UPW, 0));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + T::NST - 1 < nsteps) load_stage(s + T::NST - 1);
-        if (in == 0 && win + 1 < w1) snext = load_scales(win + 1);
+    auto read_frags = [&](MxFrags<T> &f, int s, int t) {
         const uint8_t *st = lds + (s % T::NST) * T::STAGE;
-        const uint8_t *sc = lds + T::SC_OFF + (int)(win & 1) * (T::SC_ROWS * 16);
+        // rows 32 apart have the same swizzle
+        const uint8_t *pa = st + arow * T::A_ROWB + swizzle<8>(arow, 4 * h + t) * 16;
+#pragma unroll
+        for (int i = 0; i < T::TM; i++) f.a[i] = *reinterpret_cast<const u32x4 *>(pa + i * 32 * T::A_ROWB);
         if constexpr (T::A_MX) {
-            int sa[T::TM], sb[T::TN];
+            const uint8_t *pw = st + T::W_OFF + wrow * T::W_ROWB + swizzle<8>(wrow, 4 * h + t) * 16;
+#pragma unroll
+            for (int j = 0; j < T::TN; j++) f.w[j] = *reinterpret_cast<const u32x4 *>(pw + j * 32 * T::W_ROWB);
+        }
+    };
+    // what a whole step needs: scales, and with bf16 A the W blocks
+    int sa[T::TM], sb[T::TN];
+    float sf[T::TN];
+    u32x4 wblk[T::TN];
+    auto read_step = [&](int s) {
+        const uint8_t *sc = lds + T::SC_OFF + ((w0 + s / T::WINDOW_STEPS) & 1) * (T::SC_ROWS * 16);
+        const int in = s % T::WINDOW_STEPS;
+        if constexpr (T::A_MX) {
 #pragma unroll
             for (int i = 0; i < T::TM; i++)
                 sa[i] = *reinterpret_cast<const int *>(sc + (arow + 32 * i) * 16 + in * 8 + h * 4);
 #pragma unroll
             for (int j = 0; j < T::TN; j++)
                 sb[j] = *reinterpret_cast<const int *>(sc + (T::SA_ROWS + wrow + 32 * j) * 16 + in * 8 + h * 4);
-            mx_kstep<T, 0>(st, arow, wrow, h, sa, sb, acc);
-            mx_kstep<T, 1>(st, arow, wrow, h, sa, sb, acc);
-            mx_kstep<T, 2>(st, arow, wrow, h, sa, sb, acc);
-            mx_kstep<T, 3>(st, arow, wrow, h, sa, sb, acc);
         } else {
-            float sb[T::TN];
+            const uint8_t *pw = lds + (s % T::NST) * T::STAGE + T::W_OFF + wrow * T::W_ROWB + swizzle<2>(wrow, h) * 16;
 #pragma unroll
-            for (int j = 0; j < T::TN; j++) sb[j] = e8m0_to_f32(sc[(wrow + 32 * j) * 16 + in * 2 + h]);
-            bf16_step<T>(st, arow, wrow, h, sb, acc);
+            for (int j = 0; j < T::TN; j++) {
+                sb[j] = sc[(wrow + 32 * j) * 16 + in * 2 + h];
+                wblk[j] = *reinterpret_cast<const u32x4 *>(pw + j * 32 * T::W_ROWB);
+            }
         }
-        if (in == T::WINDOW_STEPS - 1 && win + 1 < w1) put_scales(win + 1, snext);
+    };
+
+    f32x16 acc[T::TM][T::TN] = {};
+    MxFrags<T> f[2];
+    put_scales(w0, load_scales(w0));
+    u32x4 snext = load_scales(min(w0 + 1, windows - 1));
+#pragma unroll
+    for (int s = 0; s < T::NST; s++) load_stage(s);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 1) * T::UPW, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_step(0);
+    read_frags(f[0], 0, 0);
+    for (int s = 0; s < nsteps; s++) {
+        // The loop's only branch stands before its first matrix instruction: with one between them the
+        // compiler moves them all behind it, and the operands of all four quarters stay live.
+        if (s % T::WINDOW_STEPS == T::WINDOW_STEPS - 1) {
+            // the next window's scales, loaded a window ago; their buffer was last read two barriers ago
+            const int win = w0 + s / T::WINDOW_STEPS;
+            put_scales(win + 1, snext);
+            snext = load_scales(min(win + 2, windows - 1));
+        }
+        if constexpr (!T::A_MX) {
+#pragma unroll
+            for (int j = 0; j < T::TN; j++) sf[j] = e8m0_to_f32((uint32_t)sb[j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        read_frags(f[1], s, 1);
+        if constexpr (T::A_MX) mx_quarter<T, 0>(f[0], sa, sb, acc);
+        else bf16_quarter<T>(f[0], 0, wblk, sf, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        read_frags(f[0], s, 2);
+        if constexpr (T::A_MX) mx_quarter<T, 1>(f[1], sa, sb, acc);
+        else bf16_quarter<T>(f[1], 1, wblk, sf, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        read_frags(f[1], s, 3);
+        if constexpr (T::A_MX) mx_quarter<T, 2>(f[0], sa, sb, acc);
+        else bf16_quarter<T>(f[0], 2, wblk, sf, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        // stage s + 1 has landed when at most the loads of the NST - 2 later stages are outstanding
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 2) * T::UPW, 0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        load_stage(s + T::NST);  // past the last step these load zeros or a part that is not read
+        int pa[T::TM], pb[T::TN];
+        u32x4 pw[T::TN];
+#pragma unroll
+        for (int i = 0; i < T::TM; i++) pa[i] = sa[i];
+#pragma unroll
+        for (int j = 0; j < T::TN; j++) {
+            pb[j] = sb[j];
+            pw[j] = wblk[j];
+        }
+        read_step(s + 1);
+        read_frags(f[0], s + 1, 0);
+        if constexpr (T::A_MX) mx_quarter<T, 3>(f[1], pa, pb, acc);
+        else bf16_quarter<T>(f[1], 3, pw, sf, acc);
+        __builtin_amdgcn_sched_barrier(0);
     }
+    // no load may be in flight into the LDS of a workgroup that has ended
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
 
     OT *c = reinterpret_cast<OT *>(p.c);
     if constexpr (SPLIT) c += (int64_t)blockIdx.y * p.M * p.N;

@@ -5,17 +5,17 @@ A thin ctypes binding over the entry points of ``include/mxfp4.h``; the package 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
 import torch
 
-from . import (_DT, _I32, _I64, _P, _SIGNATURES, _RESTYPES, _SZ, NVFP4Tensor, _check, _ptr, _rows, _stream, _workspace,
-               check_flags, load_library)
+from . import (_DT, _I32, _I64, _P, _SIGNATURES, _RESTYPES, _SZ, _check, _rows, _workspace, check_flags,
+               load_library)
 
 MX_OP_GEMM_BF16, MX_OP_GEMM_MX, MX_OP_MOE = 0, 1, 2
 MX_BLOCK = 32
+SKINNY_MAX_M = 64  # products of up to this many rows take no workspace
 MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 64, 512, 16
 MX_EXPORTED = ["mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_moe", "mxfp4_workspace_size"]
 
@@ -58,36 +58,55 @@ class MXFP4Tensor:
                            torch.empty((rows, cols // MX_BLOCK), dtype=torch.uint8, device=device))
 
     def c(self) -> CMXTensor:
-        r, c = self.shape
-        assert c % MX_BLOCK == 0 and tuple(self.scales.shape) == (r, c // MX_BLOCK), \
-            f"MXFP4 scales: shape {tuple(self.scales.shape)}, expected {(r, c // MX_BLOCK)}"
-        for t in (self.codes, self.scales):
-            assert t.is_cuda and t.dtype == torch.uint8 and t.device == self.codes.device, \
-                "MXFP4 codes and scales must be uint8 device tensors on one device"
-            assert t.is_contiguous(), "MXFP4 codes and scales must be dense"
-        return CMXTensor(self.codes.data_ptr(), self.scales.data_ptr(), r, c)
+        codes, scales = self.codes, self.scales
+        r, half = codes.shape
+        assert half % (MX_BLOCK // 2) == 0 and scales.shape == (r, half // (MX_BLOCK // 2)), \
+            f"MXFP4 scales: shape {tuple(scales.shape)}, expected {(r, half / (MX_BLOCK // 2))}"
+        assert codes.is_cuda and codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and \
+            scales.device == codes.device, "MXFP4 codes and scales must be uint8 device tensors on one device"
+        assert codes.is_contiguous() and scales.is_contiguous(), "MXFP4 codes and scales must be dense"
+        return CMXTensor(codes.data_ptr(), scales.data_ptr(), r, half * 2)
 
 
-def _on(device: torch.device):
-    """Make `device` current for a call: the library launches on the current device."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The binding's own time is most of a small call's, so it takes the raw current stream of the device and
+# switches devices only when the tensors are not on the current one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        assert t is None or (t.is_cuda and t.device == device), f"{name}: expected a tensor on {device}"
+def _call(name: str, device: torch.device, *args) -> None:
+    """Call entry point `name` with `args` and the current stream of `device`.  The library launches on
+    the current device, so `device` is made current for the call if it is not."""
+    fn = getattr(load_library(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        _check(status, name)
+
+
+def _opt(t: torch.Tensor | None, device: torch.device, name: str, dtype: torch.dtype | None = None):
+    """Address of an optional tensor argument on `device`."""
+    if t is None:
+        return None
+    assert t.device == device and (dtype is None or t.dtype is dtype), f"{name}: {t.dtype} on {t.device}"
+    return t.data_ptr()
+
+
+def _nbytes(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _out(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype, device, what: str):
-    """The output matrix (allocated when not given) and its row stride."""
-    assert dtype in (torch.float32, torch.bfloat16), f"{what}: dtype {dtype} not offered"
+    """The output matrix (allocated when not given), its row stride and the C dtype."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    _same_device(device, **{what: out})
-    assert out.dtype == dtype and out.shape[0] == rows, f"{what}: {tuple(out.shape)} {out.dtype}"
-    return out, _rows(out, what, cols)
+        assert dtype is torch.float32 or dtype is torch.bfloat16, f"{what}: dtype {dtype} not offered"
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols, _DT[dtype]
+    assert out.device == device and out.dtype in (torch.float32, torch.bfloat16) and out.shape[0] == rows, \
+        f"{what}: {tuple(out.shape)} {out.dtype} on {out.device}"
+    return out, _rows(out, what, cols), _DT[out.dtype]
 
 
 def mx_workspace_size(op: int, m: int, n: int, k: int) -> int:
@@ -103,19 +122,15 @@ def mx_quantize(x: torch.Tensor, src_scale: torch.Tensor | None = None, flags: t
     call ORs bit 0 into on non-finite input.  check: synchronise and raise on non-finite input."""
     ld = _rows(x, "x")
     rows, cols = x.shape
+    dev = x.device
     if out is None:
-        out = MXFP4Tensor.empty(rows, cols, x.device)
-    assert out.shape == (rows, cols), f"out: shape {out.shape}, expected {(rows, cols)}"
+        out = MXFP4Tensor.empty(rows, cols, dev)
+    elif out.shape != (rows, cols) or out.codes.device != dev:
+        raise AssertionError(f"out: shape {out.shape} on {out.codes.device}, expected {(rows, cols)} on {dev}")
     if flags is None and check:
-        flags = torch.zeros(1, dtype=torch.int32, device=x.device)
-    _same_device(x.device, src_scale=src_scale, flags=flags, out=out.codes)
-    assert src_scale is None or src_scale.dtype == torch.float32
-    assert flags is None or flags.dtype == torch.int32
-    ct = out.c()
-    with _on(x.device):
-        st = load_library().mxfp4_quantize(_ptr(x), _DT[x.dtype], ld, _ptr(src_scale), ctypes.byref(ct), _ptr(flags),
-                                           _stream(x.device))
-    _check(st, "mxfp4_quantize")
+        flags = torch.zeros(1, dtype=torch.int32, device=dev)
+    _call("mxfp4_quantize", dev, x.data_ptr(), _DT[x.dtype], ld, _opt(src_scale, dev, "src_scale", torch.float32),
+          ctypes.byref(out.c()), _opt(flags, dev, "flags", torch.int32))
     out.flags = flags
     if check:
         check_flags(flags, "mxfp4_quantize")
@@ -126,19 +141,23 @@ def mx_dequantize(q: MXFP4Tensor, dtype: torch.dtype = torch.bfloat16, out: torc
     """Expand MXFP4 to bf16 or fp32 (exact)."""
     rows, cols = q.shape
     dev = q.codes.device
-    out, ld = _out(out, rows, cols, dtype if out is None else out.dtype, dev, "out")
-    ct = q.c()
-    with _on(dev):
-        st = load_library().mxfp4_dequantize(ctypes.byref(ct), _ptr(out), _DT[out.dtype], ld, _stream(dev))
-    _check(st, "mxfp4_dequantize")
+    out, ld, dt = _out(out, rows, cols, dtype, dev, "out")
+    _call("mxfp4_dequantize", dev, ctypes.byref(q.c()), out.data_ptr(), dt, ld)
     return out
+
+
+def _gemm_workspace(op: int, m: int, n: int, k: int, device: torch.device) -> torch.Tensor | None:
+    if device.index == torch.cuda.current_device():  # the size is planned for the current device
+        return _workspace(mx_workspace_size(op, m, n, k), device)
+    with torch.cuda.device(device.index):
+        return _workspace(mx_workspace_size(op, m, n, k), device)
 
 
 def mx_gemm_workspace(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor) -> torch.Tensor | None:
     """A workspace for mx_gemm(a, w), for callers that keep one (None when the product needs none).  Its
     contents do not matter; calls that share one must be ordered (same stream, or events)."""
     op = MX_OP_GEMM_MX if isinstance(a, MXFP4Tensor) else MX_OP_GEMM_BF16
-    return _workspace(mx_workspace_size(op, a.shape[0], w.shape[0], w.shape[1]), w.codes.device)
+    return _gemm_workspace(op, a.shape[0], w.shape[0], w.shape[1], w.codes.device)
 
 
 def mx_gemm(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor, dtype: torch.dtype = torch.float32,
@@ -146,29 +165,22 @@ def mx_gemm(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor, dtype: torch.dtype = 
     """C [M, N] (fp32 or bf16) = A . W^T with MXFP4 weights [N, K].  `a` is an MXFP4Tensor [M, K] (W4A4: FP4
     matrix instructions) or a bf16 tensor [M, K] (W4A16).  fp32 sums, rounded once."""
     assert isinstance(w, MXFP4Tensor), "w: an MXFP4Tensor is required"
-    assert not isinstance(a, NVFP4Tensor), "a: NVFP4 activations do not go with MXFP4 weights"
     n, k = w.shape
     dev = w.codes.device
     m = a.shape[0]
     if isinstance(a, MXFP4Tensor):
-        assert a.shape[1] == k, f"a: {a.shape[1]} columns, expected {k}"
-        _same_device(dev, a=a.codes)
-        a_ct, a_ptr, lda = ctypes.byref(a.c()), None, k
+        assert a.shape[1] == k and a.codes.device == dev, f"a: {a.shape} on {a.codes.device}, expected {k} columns on {dev}"
+        a_ct, a_ptr, lda, op = ctypes.byref(a.c()), None, k, MX_OP_GEMM_MX
     else:
-        assert a.dtype == torch.bfloat16, f"a: bf16 or MXFP4, not {a.dtype}"
-        _same_device(dev, a=a)
+        assert isinstance(a, torch.Tensor) and a.dtype is torch.bfloat16 and a.device == dev, \
+            f"a: a bf16 tensor or an MXFP4Tensor on {dev} is required"
         lda = _rows(a, "a", k)
-        a_ct, a_ptr = None, _ptr(a)
-    out, ldc = _out(out, m, n, dtype if out is None else out.dtype, dev, "out")
-    wct = w.c()
-    lib = load_library()
-    with _on(dev):
-        if workspace is None:
-            workspace = mx_gemm_workspace(a, w)
-        _same_device(dev, workspace=workspace)
-        st = lib.mxfp4_gemm(a_ptr, a_ct, m, lda, ctypes.byref(wct), _ptr(out), _DT[out.dtype], ldc, _ptr(workspace),
-                            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev))
-    _check(st, "mxfp4_gemm")
+        a_ct, a_ptr, op = None, a.data_ptr(), MX_OP_GEMM_BF16
+    out, ldc, dt = _out(out, m, n, dtype, dev, "out")
+    if workspace is None and m > SKINNY_MAX_M:  # none needed below
+        workspace = _gemm_workspace(op, m, n, k, dev)
+    _call("mxfp4_gemm", dev, a_ptr, a_ct, m, lda, ctypes.byref(w.c()), out.data_ptr(), dt, ldc,
+          _opt(workspace, dev, "workspace"), _nbytes(workspace))
     return out
 
 
@@ -190,26 +202,20 @@ def mx_moe(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_down
     chosen entries of the softmax over all of them.  Returns y [T, H], or with routing=True (y, ids,
     weights): ids [T, top_k] int32 in descending order of logit and their p, -1 and 0 where a row has fewer."""
     dev = x.device
-    assert x.dtype == torch.bfloat16, f"x: bf16, not {x.dtype}"
+    assert x.dtype is torch.bfloat16, f"x: bf16, not {x.dtype}"
     assert logits.dtype in (torch.float32, torch.bfloat16), f"logits: fp32 or bf16, not {logits.dtype}"
     ld_x, ld_l = _rows(x, "x", w_gate_up.shape[1]), _rows(logits, "logits")
     t, h = x.shape
     assert logits.shape[0] == t, f"logits: {logits.shape[0]} rows, expected {t}"
-    _same_device(dev, logits=logits, w_gate_up=w_gate_up.codes, w_down=w_down.codes)
-    out, ld_y = _out(out, t, h, dtype if out is None else out.dtype, dev, "out")
+    assert logits.device == dev and w_gate_up.codes.device == dev and w_down.codes.device == dev, "one device per call"
+    out, ld_y, dt = _out(out, t, h, dtype, dev, "out")
     ids = weights = None
     if routing:
         ids = torch.empty((t, top_k), dtype=torch.int32, device=dev)
         weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
-    gct, dct = w_gate_up.c(), w_down.c()
-    with _on(dev):
-        if workspace is None:
-            workspace = mx_moe_workspace(t, top_k, w_down)
-        _same_device(dev, workspace=workspace)
-        st = load_library().mxfp4_moe(_ptr(x), t, ld_x, _ptr(logits), _DT[logits.dtype], ld_l, logits.shape[1], top_k,
-                                      1 if renormalize else 0, ctypes.byref(gct), ctypes.byref(dct), _ptr(out),
-                                      _DT[out.dtype], ld_y, _ptr(ids), _ptr(weights), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                      _stream(dev))
-    _check(st, "mxfp4_moe")
+    if workspace is None:
+        workspace = mx_moe_workspace(t, top_k, w_down)
+    _call("mxfp4_moe", dev, x.data_ptr(), t, ld_x, logits.data_ptr(), _DT[logits.dtype], ld_l, logits.shape[1], top_k,
+          1 if renormalize else 0, ctypes.byref(w_gate_up.c()), ctypes.byref(w_down.c()), out.data_ptr(), dt, ld_y,
+          _opt(ids, dev, "ids"), _opt(weights, dev, "weights"), _opt(workspace, dev, "workspace"), _nbytes(workspace))
     return (out, ids, weights) if routing else out
