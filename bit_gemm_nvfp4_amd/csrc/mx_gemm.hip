@@ -158,6 +158,11 @@ struct MxTile {
     static constexpr int LDS_BYTES = SC_OFF + 2 * SC_ROWS * 16;
     static constexpr int UNITS = STAGE / 1024, A_UNITS = W_OFF / 1024, UPW = UNITS / NW;
     static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    static constexpr int READS = TM + (A_MX ? TN : 0);  // LDS reads of a quarter's operands
+    // epilogue: 32 rows of a wave's columns; rows 4 apart start 32 banks apart, so that the two halves of a
+    // wave write different banks
+    static constexpr int EPI_ROW = WTN + 8, EPI_BYTES = 32 * EPI_ROW * 4;
+    static_assert((4 * EPI_ROW) % 64 == 32 && NW * EPI_BYTES <= LDS_BYTES, "epilogue rows");
     static_assert(NW % 2 == 0, "the units of a wave share a swizzle");
     static_assert(STAGE % 1024 == 0 && UNITS % NW == 0 && A_UNITS % NW == 0 && SC_ROWS <= NT, "tile shape");
     static_assert(LDS_BYTES <= 160 * 1024 && NST >= 2, "LDS stages");
@@ -217,6 +222,7 @@ struct MxTileArgs {
     int64_t ldc;
     int tiles_m, tiles_n;
     int slice_windows;  // windows of 512 columns per K slice (blockIdx.y)
+    int vec_c;          // rows of C (of the partial planes) are 16-byte aligned
 };
 
 // Operands of one quarter of a step, and its matrix instructions.
@@ -252,13 +258,35 @@ __device__ __forceinline__ void bf16_quarter(const MxFrags<T> &f, int q, const u
                                                                 0, 0, 0);
 }
 
+// Keeps the matrix instructions issued so far above this point: the accumulators pass through an empty
+// statement.
+template <class T>
+__device__ __forceinline__ void pin(f32x16 (&acc)[T::TM][T::TN]) {
+#pragma unroll
+    for (int i = 0; i < T::TM; i++)
+#pragma unroll
+        for (int j = 0; j < T::TN; j++) asm volatile("" : "+v"(acc[i][j]));
+}
+
+// Instruction order of a quarter: two LDS reads behind each of the first matrix instructions, so that the
+// next quarter's operands have most of this quarter to arrive in.
+template <class T, int READS>
+__device__ __forceinline__ void order_quarter() {
+#pragma unroll
+    for (int r = 0; r < READS / 2; r++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, T::TM * T::TN, 0);
+}
+
 // The main loop runs in quarters of a step with the operands of the next quarter read from LDS while the
 // matrix instructions of this one issue.  The step's one barrier stands before its last quarter, whose
 // operands are then in registers: behind it stage s + 1 is complete in LDS, so the first operands of
 // step s + 1 are read under the last quarter's instructions, and stage s may be overwritten, so the
 // loads of step s + NST are issued.
 template <class T, class OT, bool SPLIT>
-__global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
+__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(MxTileArgs p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
     int tm, tn;
     if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn)) return;
@@ -310,17 +338,17 @@ __global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
     };
 
     const int arow = (wave / T::WN) * T::WTM + (lane & 31), wrow = (wave % T::WN) * T::WTN + (lane & 31);
+    // in the order of use: the first matrix instruction takes w[0] and a[0]
     auto read_frags = [&](MxFrags<T> &f, int s, int t) {
         const uint8_t *st = lds + (s % T::NST) * T::STAGE;
-        // rows 32 apart have the same swizzle
-        const uint8_t *pa = st + arow * T::A_ROWB + swizzle<8>(arow, 4 * h + t) * 16;
-#pragma unroll
-        for (int i = 0; i < T::TM; i++) f.a[i] = *reinterpret_cast<const u32x4 *>(pa + i * 32 * T::A_ROWB);
-        if constexpr (T::A_MX) {
+        if constexpr (T::A_MX) {  // rows 32 apart have the same swizzle
             const uint8_t *pw = st + T::W_OFF + wrow * T::W_ROWB + swizzle<8>(wrow, 4 * h + t) * 16;
 #pragma unroll
             for (int j = 0; j < T::TN; j++) f.w[j] = *reinterpret_cast<const u32x4 *>(pw + j * 32 * T::W_ROWB);
         }
+        const uint8_t *pa = st + arow * T::A_ROWB + swizzle<8>(arow, 4 * h + t) * 16;
+#pragma unroll
+        for (int i = 0; i < T::TM; i++) f.a[i] = *reinterpret_cast<const u32x4 *>(pa + i * 32 * T::A_ROWB);
     };
     // what a whole step needs: scales, and with bf16 A the W blocks
     int sa[T::TM], sb[T::TN];
@@ -374,14 +402,20 @@ __global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
         read_frags(f[1], s, 1);
         if constexpr (T::A_MX) mx_quarter<T, 0>(f[0], sa, sb, acc);
         else bf16_quarter<T>(f[0], 0, wblk, sf, acc);
+        pin<T>(acc);
+        order_quarter<T, T::READS>();
         __builtin_amdgcn_sched_barrier(0);
         read_frags(f[0], s, 2);
         if constexpr (T::A_MX) mx_quarter<T, 1>(f[1], sa, sb, acc);
         else bf16_quarter<T>(f[1], 1, wblk, sf, acc);
+        pin<T>(acc);
+        order_quarter<T, T::READS>();
         __builtin_amdgcn_sched_barrier(0);
         read_frags(f[1], s, 3);
         if constexpr (T::A_MX) mx_quarter<T, 2>(f[0], sa, sb, acc);
         else bf16_quarter<T>(f[0], 2, wblk, sf, acc);
+        pin<T>(acc);
+        order_quarter<T, T::READS>();
         __builtin_amdgcn_sched_barrier(0);
         // stage s + 1 has landed when at most the loads of the NST - 2 later stages are outstanding
         __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 2) * T::UPW, 0));
@@ -401,6 +435,8 @@ __global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
         read_frags(f[0], s + 1, 0);
         if constexpr (T::A_MX) mx_quarter<T, 3>(f[1], pa, pb, acc);
         else bf16_quarter<T>(f[1], 3, pw, sf, acc);
+        pin<T>(acc);
+        order_quarter<T, T::READS + (T::A_MX ? (T::TM + T::TN + 1) / 2 : 2 * T::TN)>();
         __builtin_amdgcn_sched_barrier(0);
     }
     // no load may be in flight into the LDS of a workgroup that has ended
@@ -408,16 +444,52 @@ __global__ __launch_bounds__(T::NT) void k_mx_tile(MxTileArgs p) {
 
     OT *c = reinterpret_cast<OT *>(p.c);
     if constexpr (SPLIT) c += (int64_t)blockIdx.y * p.M * p.N;
+    const int64_t ldc = SPLIT ? p.N : p.ldc;
+    const int64_t mw = m0 + (wave / T::WN) * T::WTM, nw = n0 + (wave % T::WN) * T::WTN;  // the wave's corner
+    constexpr int VEC = 16 / sizeof(OT);
+    // Each lane holds single elements of many rows (column l % 32), and a store instruction takes 16
+    // cycles whatever its width, so 32 rows at a time pass through LDS (free now, a part per wave) and leave
+    // as 16 bytes per lane: a quarter (fp32) or an eighth (bf16) of the stores.  4096 x 4096 x 8192 W4A4, fp32
+    // C: 76.0 us with single-element stores.
+    if (n0 + T::BN <= p.N && p.vec_c) {
+        __syncthreads();  // the other waves have read their last operands
+        float *buf = reinterpret_cast<float *>(lds + wave * T::EPI_BYTES);
+#pragma unroll
+        for (int i = 0; i < T::TM; i++) {
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+#pragma unroll
+                for (int j = 0; j < T::TN; j++)
+                    buf[(8 * (e / 4) + 4 * h + e % 4) * T::EPI_ROW + 32 * j + (lane & 31)] = acc[i][j][e];
+            constexpr int LPR = T::WTN / VEC, RPI = 64 / LPR;  // lanes per row, rows per instruction
+#pragma unroll
+            for (int q = 0; q < 32 / RPI; q++) {
+                const int row = q * RPI + lane / LPR, col = lane % LPR * VEC;
+                const float *src = buf + row * T::EPI_ROW + col;
+                const int64_t m = mw + 32 * i + row;
+                if constexpr (VEC == 4) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+                    if (m < p.M) *reinterpret_cast<f32x4 *>(c + m * ldc + nw + col) = v;
+                } else {
+                    const f32x4 u = *reinterpret_cast<const f32x4 *>(src), w = *reinterpret_cast<const f32x4 *>(src + 4);
+                    const bf16x8 v{(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
+                                   (__bf16)w[0], (__bf16)w[1], (__bf16)w[2], (__bf16)w[3]};
+                    if (m < p.M) *reinterpret_cast<bf16x8 *>(c + m * ldc + nw + col) = v;
+                }
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < T::TM; i++)
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-            const int64_t m = m0 + (wave / T::WN) * T::WTM + 32 * i + 8 * (e / 4) + 4 * h + e % 4;
+            const int64_t m = mw + 32 * i + 8 * (e / 4) + 4 * h + e % 4;
             if (m >= p.M) continue;
 #pragma unroll
             for (int j = 0; j < T::TN; j++) {
-                const int64_t n = n0 + wrow + 32 * j;
-                if (n < p.N) store_out(c + m * (SPLIT ? p.N : p.ldc) + n, acc[i][j][e]);
+                const int64_t n = nw + 32 * j + (lane & 31);
+                if (n < p.N) store_out(c + m * ldc + n, acc[i][j][e]);
             }
         }
 }
@@ -481,11 +553,13 @@ void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) 
     const int per = (p.tiles_m * p.tiles_n + 7) / 8;
     const dim3 grid(per * 8, splits);
     if (splits == 1) {
+        p.vec_c = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc * sizeof(OT) % 16 == 0;
         hipLaunchKernelGGL((k_mx_tile<T, OT, false>), grid, dim3(T::NT), 0, stream, p);
         return;
     }
     OT *c = reinterpret_cast<OT *>(p.c);
     p.c = partial;
+    p.vec_c = p.N % 4 == 0;
     hipLaunchKernelGGL((k_mx_tile<T, float, true>), grid, dim3(T::NT), 0, stream, p);
     const int64_t blocks = std::min<int64_t>((p.M * p.N + 255) / 256, 8192);
     hipLaunchKernelGGL(k_mx_reduce<OT>, dim3((unsigned)blocks), dim3(256), 0, stream,
