@@ -154,7 +154,7 @@ struct MxTile {
     static constexpr int W_OFF = BM * A_ROWB, STAGE = W_OFF + BN * W_ROWB;
     static constexpr int NST = NST_;
     static constexpr int WINDOW_STEPS = kGroup / BK;
-    static constexpr int SA_ROWS = A_MX ? BM : 0, SC_ROWS = SA_ROWS + BN, SC_OFF = NST * STAGE;
+    static constexpr int SA_ROWS = A_MX ? BM : 0, SC_ROWS = SA_ROWS + BN, SC_PER = (SC_ROWS + NT - 1) / NT, SC_OFF = NST * STAGE;
     static constexpr int LDS_BYTES = SC_OFF + 2 * SC_ROWS * 16;
     static constexpr int UNITS = STAGE / 1024, A_UNITS = W_OFF / 1024, UPW = UNITS / NW;
     static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
@@ -164,7 +164,7 @@ struct MxTile {
     static constexpr int EPI_ROW = WTN + 8, EPI_BYTES = 32 * EPI_ROW * 4;
     static_assert((4 * EPI_ROW) % 64 == 32 && NW * EPI_BYTES <= LDS_BYTES, "epilogue rows");
     static_assert(NW % 2 == 0, "the units of a wave share a swizzle");
-    static_assert(STAGE % 1024 == 0 && UNITS % NW == 0 && A_UNITS % NW == 0 && SC_ROWS <= NT, "tile shape");
+    static_assert(STAGE % 1024 == 0 && UNITS % NW == 0 && A_UNITS % NW == 0, "tile shape");
     static_assert(LDS_BYTES <= 160 * 1024 && NST >= 2, "LDS stages");
 };
 
@@ -324,17 +324,30 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
             else load_to_lds16(rw, dst + i * (T::NW * 1024), wv, wo + (i - A_PER) * (T::NW * RPU) * wrb);
         }
     };
-    // scale rows: thread tid < SC_ROWS serves row tid of [A rows (MXFP4 A), W rows]
-    const uint8_t *srow = nullptr;
-    if (tid < T::SA_ROWS) {
-        if (tid < mrows) srow = p.ascales + (m0 + tid) * (int64_t)kb;
-    } else if (tid < T::SC_ROWS) {
-        if (tid - T::SA_ROWS < nrows) srow = p.wscales + (n0 + tid - T::SA_ROWS) * (int64_t)kb;
+    // scale rows [A rows (MXFP4 A), W rows]: thread tid serves rows tid, tid + NT, ...
+    const uint8_t *srow[T::SC_PER];
+#pragma unroll
+    for (int i = 0; i < T::SC_PER; i++) {
+        const int r = tid + i * T::NT;
+        srow[i] = nullptr;
+        if (r < T::SA_ROWS) {
+            if (r < mrows) srow[i] = p.ascales + (m0 + r) * (int64_t)kb;
+        } else if (r < T::SC_ROWS) {
+            if (r - T::SA_ROWS < nrows) srow[i] = p.wscales + (n0 + r - T::SA_ROWS) * (int64_t)kb;
+        }
     }
-    auto load_scales = [&](int w) { return srow ? load_scale_window(srow, w, kb) : u32x4{0, 0, 0, 0}; };
-    auto put_scales = [&](int w, u32x4 v) {
-        if (tid < T::SC_ROWS)
-            *reinterpret_cast<u32x4 *>(lds + T::SC_OFF + (w & 1) * (T::SC_ROWS * 16) + tid * 16) = v;
+    u32x4 snext[T::SC_PER];
+    auto load_scales = [&](int w) {
+#pragma unroll
+        for (int i = 0; i < T::SC_PER; i++)
+            snext[i] = srow[i] ? load_scale_window(srow[i], w, kb) : u32x4{0, 0, 0, 0};
+    };
+    auto put_scales = [&](int w) {
+#pragma unroll
+        for (int i = 0; i < T::SC_PER; i++)
+            if (T::SC_ROWS % T::NT == 0 || tid + i * T::NT < T::SC_ROWS)
+                *reinterpret_cast<u32x4 *>(lds + T::SC_OFF + (w & 1) * (T::SC_ROWS * 16) + (tid + i * T::NT) * 16) =
+                    snext[i];
     };
 
     const int arow = (wave / T::WN) * T::WTM + (lane & 31), wrow = (wave % T::WN) * T::WTN + (lane & 31);
@@ -376,8 +389,9 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
 
     f32x16 acc[T::TM][T::TN] = {};
     MxFrags<T> f[2];
-    put_scales(w0, load_scales(w0));
-    u32x4 snext = load_scales(min(w0 + 1, windows - 1));
+    load_scales(w0);
+    put_scales(w0);
+    load_scales(min(w0 + 1, windows - 1));
 #pragma unroll
     for (int s = 0; s < T::NST; s++) load_stage(s);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 1) * T::UPW, 0));
@@ -391,8 +405,8 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         if (s % T::WINDOW_STEPS == T::WINDOW_STEPS - 1) {
             // the next window's scales, loaded a window ago; their buffer was last read two barriers ago
             const int win = w0 + s / T::WINDOW_STEPS;
-            put_scales(win + 1, snext);
-            snext = load_scales(min(win + 2, windows - 1));
+            put_scales(win + 1);
+            load_scales(min(win + 2, windows - 1));
         }
         if constexpr (!T::A_MX) {
 #pragma unroll
@@ -449,8 +463,8 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     constexpr int VEC = 16 / sizeof(OT);
     // Each lane holds single elements of many rows (column l % 32), and a store instruction takes 16
     // cycles whatever its width, so 32 rows at a time pass through LDS (free now, a part per wave) and leave
-    // as 16 bytes per lane: a quarter (fp32) or an eighth (bf16) of the stores.  4096 x 4096 x 8192 W4A4, fp32
-    // C: 76.0 us with single-element stores.
+    // as 16 bytes per lane: a quarter (fp32) or an eighth (bf16) of the stores.  W4A4 4096 x 12288 x 4096 with
+    // bf16 C 131 -> 118 us; with fp32 C, which HBM bounds, 133 -> 131 us.
     if (n0 + T::BN <= p.N && p.vec_c) {
         __syncthreads();  // the other waves have read their last operands
         float *buf = reinterpret_cast<float *>(lds + wave * T::EPI_BYTES);
@@ -517,26 +531,47 @@ __global__ __launch_bounds__(256) void k_mx_zero(OT *C, int64_t M, int64_t N, in
 // launches
 // -------------------------------------------------------------------------------------------------
 struct MxPlan {
-    int cfg;            // 0: 256-row tiles, 1: 128-row tiles
+    int cfg;            // index into the tile shapes
     int splits;         // K slices
     int slice_windows;  // windows of 512 columns per slice
 };
 
+// Tile shapes and what they cost: microseconds per tile (start, first loads, stores) and per window of 512
+// columns, with one workgroup per CU and with `per_cu` of them.  Fitted to timings of every shape with 1, 2
+// and 4 K slices on an MI355X; of those, in microseconds (tile: time; the shape picked is marked):
+//   W4A4   512 x 12288 x 4096   256x256: 33.1   128x256: 23.8 *  128x128: 29.9   64x128: 34.6
+//   W4A4   512 x 4096 x 12288   256x256: 81.5   128x256: 52.2    128x128 in two slices: 31.1 * (one: 35.8)
+//   W4A4   4096 x 4096 x 4096   256x256: 40.1 * 128x256: 45.2    128x128: 54.1   64x128: 60.8
+//   W4A4   200 x 1000 x 2048    256x256: 19.4   128x256: 13.7    128x128: 9.2 *  64x128: 7.6
+//   W4A16  512 x 12288 x 4096   256x256: 81.4   128x256: 50.1 *  128x128: 55.5   64x128: 60.3
+//   W4A16  512 x 4096 x 12288   128x256: 128.4, in four slices 59.1 *  128x128 in two: 64.2
+//   W4A16  128 x 4096 x 4096    128x128: 35.6   64x128: 26.5, in four slices 17.9 *
+//   W4A16  4096 x 12288 x 4096  256x256: 313 *  128x256: 359     128x128: 361
+struct TileCost {
+    int bm, bn, per_cu;
+    double start, window, window_full;
+};
+constexpr TileCost kTileCost[2][4] = {
+    {{256, 256, 1, 3.0, 12.6, 12.6}, {128, 256, 1, 5.0, 6.4, 6.4}, {128, 128, 2, 4.0, 4.0, 7.0}, {64, 128, 2, 3.0, 2.95, 4.5}},
+    {{256, 256, 1, 7.8, 3.84, 3.84}, {128, 256, 1, 5.0, 2.5, 2.5}, {128, 128, 1, 2.5, 1.45, 1.45}, {64, 128, 2, 2.5, 1.6, 1.8}},
+};
 constexpr int kMaxSplits = 8;
+constexpr double kReduceStart = 4.0, kReduceBytesPerUs = 3.0e6;  // the pass that adds the slices
 
 MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
     const int64_t windows = (K + kGroup - 1) / kGroup;
     MxPlan best{0, 1, (int)windows};
     double cost = 1e30;
-    for (int cfg = 0; cfg < 2; cfg++) {
-        const int bm = cfg == 0 ? 256 : 128, bn = bm;
-        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+    for (int cfg = 0; cfg < 4; cfg++) {
+        const TileCost &t = kTileCost[a_mx ? 1 : 0][cfg];
+        const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
         for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplits, windows); s++) {
-            const int64_t per = (windows + s - 1) / s, used = (windows + per - 1) / per;
-            if (used != s) continue;
-            const double rounds = (double)((tiles * s + num_cus - 1) / num_cus);
-            double us = rounds * (per * bm * bn * (cfg == 0 ? 1.0 : 1.4) * 3.5e-5 * (a_mx ? 1.0 : 4.0) + 3.0);
-            if (s > 1) us += 4.0 + (double)M * N * 4 * (s + 1) / 4.0e6;
+            const int64_t per = (windows + s - 1) / s;
+            if ((windows + per - 1) / per != s) continue;  // a slice would be empty
+            const int64_t all = tiles * s, slots = (int64_t)num_cus * t.per_cu;
+            double us = all <= num_cus ? t.start + per * t.window
+                                       : (double)((all + slots - 1) / slots) * (t.start + per * t.window_full);
+            if (s > 1) us += kReduceStart + (double)M * N * 4 * (s + 1) / kReduceBytesPerUs;
             if (us < cost) {
                 cost = us;
                 best = MxPlan{cfg, (int)s, (int)per};
@@ -589,11 +624,19 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
     }
     p.slice_windows = plan.slice_windows;
     if (a_mx) {
-        if (plan.cfg == 0) launch_tile_t<MxTile<256, 256, 2, 4, true, 2>, OT>(p, plan.splits, workspace, stream);
-        else launch_tile_t<MxTile<128, 128, 2, 2, true, 2>, OT>(p, plan.splits, workspace, stream);
+        switch (plan.cfg) {
+        case 0: launch_tile_t<MxTile<256, 256, 2, 4, true, 2>, OT>(p, plan.splits, workspace, stream); break;
+        case 1: launch_tile_t<MxTile<128, 256, 2, 4, true, 3>, OT>(p, plan.splits, workspace, stream); break;
+        case 2: launch_tile_t<MxTile<128, 128, 4, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
+        default: launch_tile_t<MxTile<64, 128, 2, 2, true, 2>, OT>(p, plan.splits, workspace, stream); break;
+        }
     } else {
-        if (plan.cfg == 0) launch_tile_t<MxTile<256, 256, 2, 4, false, 3>, OT>(p, plan.splits, workspace, stream);
-        else launch_tile_t<MxTile<128, 128, 2, 2, false, 3>, OT>(p, plan.splits, workspace, stream);
+        switch (plan.cfg) {
+        case 0: launch_tile_t<MxTile<256, 256, 2, 4, false, 3>, OT>(p, plan.splits, workspace, stream); break;
+        case 1: launch_tile_t<MxTile<128, 256, 2, 4, false, 3>, OT>(p, plan.splits, workspace, stream); break;
+        case 2: launch_tile_t<MxTile<128, 128, 2, 2, false, 3>, OT>(p, plan.splits, workspace, stream); break;
+        default: launch_tile_t<MxTile<64, 128, 1, 4, false, 4>, OT>(p, plan.splits, workspace, stream); break;
+        }
     }
 }
 
