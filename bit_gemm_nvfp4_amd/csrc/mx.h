@@ -37,31 +37,36 @@ struct MxGroup {
     u32x4 s;
 };
 
-// codes and scales point at the lane's row.  nblk: blocks of the row from the start of the group on.
-__device__ __forceinline__ MxGroup load_mx_group(const uint8_t *codes, const uint8_t *scales, int64_t grp, int lg,
-                                                 int64_t nblk) {
+// codes and scales point at the lane's row.
+__device__ __forceinline__ MxGroup load_mx_group(const uint8_t *codes, const uint8_t *scales, int grp, int lg) {
     MxGroup r;
-    const uint8_t *cp = codes + grp * (kGroup / 2) + lg * 16;
-    const uint8_t *sp = scales + grp * kGroupBlocks;
-    if (nblk >= kGroupBlocks) {
+    const uint8_t *cp = codes + (int64_t)grp * (kGroup / 2) + lg * 16;
 #pragma unroll
-        for (int i = 0; i < kGroupChunks; i++) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
-        r.s = *reinterpret_cast<const u32x4_u *>(sp);
-    } else {  // the last, partial group: blocks past the row's end read as zero codes with scale 2^-127
+    for (int i = 0; i < kGroupChunks; i++) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
+    r.s = *reinterpret_cast<const u32x4_u *>(scales + (int64_t)grp * kGroupBlocks);
+    return r;
+}
+
+// The last, partial group (nblk < kGroupBlocks blocks are left): blocks past the row's end read as zero
+// codes with scale 2^-127.
+__device__ __forceinline__ MxGroup load_mx_tail(const uint8_t *codes, const uint8_t *scales, int grp, int lg,
+                                                int nblk) {
+    MxGroup r;
+    const uint8_t *cp = codes + (int64_t)grp * (kGroup / 2) + lg * 16;
+    const uint8_t *sp = scales + (int64_t)grp * kGroupBlocks;
 #pragma unroll
-        for (int i = 0; i < kGroupChunks; i++) {
-            r.c[i] = u32x4{0, 0, 0, 0};
-            if (i * 4 + lg < nblk) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
-        }
-        uint32_t s[4] = {0, 0, 0, 0};
-        for (int b = 0; b < (int)nblk; b++) {
-            const uint32_t v = sp[b];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                if (b / 4 == i) s[i] |= v << (8 * (b % 4));
-        }
-        r.s = u32x4{s[0], s[1], s[2], s[3]};
+    for (int i = 0; i < kGroupChunks; i++) {
+        r.c[i] = u32x4{0, 0, 0, 0};
+        if (i * 4 + lg < nblk) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
     }
+    uint32_t s[4] = {0, 0, 0, 0};
+    for (int b = 0; b < nblk; b++) {
+        const uint32_t v = sp[b];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (b / 4 == i) s[i] |= v << (8 * (b % 4));
+    }
+    r.s = u32x4{s[0], s[1], s[2], s[3]};
     return r;
 }
 
@@ -78,6 +83,45 @@ __device__ __forceinline__ bf16x8 fp4_to_bf16x8(uint32_t w, float scale) {
 
 __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// The bf16 operand of a group: lane l holds block l / 16 of each chunk of row l % 16, 32 values.
+struct Bf16Group {
+    u32x4 v[kGroupChunks][4];
+};
+
+__device__ __forceinline__ Bf16Group load_bf16_group(const __bf16 *row, int grp, int lg) {
+    Bf16Group r;
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (int64_t)grp * kGroup + lg * kMxBlock);
+#pragma unroll
+    for (int i = 0; i < kGroupChunks; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) r.v[i][j] = p[i * 16 + j];
+    return r;
+}
+
+__device__ __forceinline__ Bf16Group load_bf16_tail(const __bf16 *row, int grp, int lg, int nblk) {
+    Bf16Group r;
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (int64_t)grp * kGroup + lg * kMxBlock);
+#pragma unroll
+    for (int i = 0; i < kGroupChunks; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            r.v[i][j] = u32x4{0, 0, 0, 0};
+            if (i * 4 + lg < nblk) r.v[i][j] = p[i * 16 + j];
+        }
+    return r;
+}
+
+// acc += W . a over a group: the lane's W blocks are expanded exactly to bf16, sixteen instructions.
+__device__ __forceinline__ void group_product(const MxGroup &w, const Bf16Group &a, int lg, f32x4 &acc) {
+#pragma unroll
+    for (int i = 0; i < kGroupChunks; i++) {
+        const float s = e8m0_to_f32((w.s[i] >> (8 * lg)) & 255u);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            acc = mfma_bf16(fp4_to_bf16x8(w.c[i][j], s), __builtin_bit_cast(bf16x8, a.v[i][j]), acc);
+    }
 }
 
 // Host side ---------------------------------------------------------------------------------------

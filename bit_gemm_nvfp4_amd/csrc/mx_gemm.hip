@@ -32,94 +32,78 @@ __device__ __forceinline__ void store_out(OT *p, float v) {
 // -------------------------------------------------------------------------------------------------
 // M <= 64
 // -------------------------------------------------------------------------------------------------
-// Activation fragments of chunk i of a group for 16 rows of A (lane: row l % 16, block l / 16).
-__device__ __forceinline__ void load_bf16_block(const __bf16 *row, int64_t blk, bool ok, bf16x8 *f) {
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (ok ? blk : 0) * kMxBlock);
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const u32x4 v = p[j];
-        const u32x4 z = u32x4{0, 0, 0, 0};
-        f[j] = __builtin_bit_cast(bf16x8, ok ? v : z);
-    }
-}
-
-template <int CT, int RT, bool A_MX, class OT>
+// The W groups of a wave are wave, wave + waves, ...; the next one's loads are issued before the current
+// one's products, so two are in flight per wave.
+template <int CT, bool A_MX, class OT>
 __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A, int64_t lda,
                                                    const uint8_t *__restrict__ acodes,
                                                    const uint8_t *__restrict__ ascales, int M,
                                                    const uint8_t *__restrict__ wcodes,
-                                                   const uint8_t *__restrict__ wscales, int64_t N, int64_t K,
+                                                   const uint8_t *__restrict__ wscales, int64_t N, int K,
                                                    OT *__restrict__ C, int64_t ldc) {
-    extern __shared__ float red[];  // [waves][RT][CT][256]
+    extern __shared__ float red[];  // [waves][CT][256]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
-    const int64_t kb = K / kMxBlock, kbytes = K / 2;
-    const uint8_t *wc[RT], *ws[RT];
-#pragma unroll
-    for (int i = 0; i < RT; i++) {  // rows past N repeat the last one; their results are not stored
-        const int64_t row = min(n0 + 16 * i + r, N - 1);
-        wc[i] = wcodes + row * kbytes;
-        ws[i] = wscales + row * kb;
-    }
-    int64_t arow[CT];
-#pragma unroll
-    for (int c = 0; c < CT; c++) arow[c] = min(c * 16 + r, M - 1);
-    f32x4 acc[RT][CT] = {};
-    const int64_t ngrp = (K + kGroup - 1) / kGroup;
-    for (int64_t g = wave; g < ngrp; g += waves) {
-        const int64_t nblk = kb - g * kGroupBlocks;
-        MxGroup w[RT];
-#pragma unroll
-        for (int i = 0; i < RT; i++) w[i] = load_mx_group(wc[i], ws[i], g, lg, nblk);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int kb = K / kMxBlock;
+    // rows past N (and past M below) repeat the last one; their results are not stored
+    const int64_t row = min(n0 + r, N - 1);
+    const uint8_t *wc = wcodes + row * (K / 2), *ws = wscales + row * kb;
+    const int full = K / kGroup, tail = kb - full * kGroupBlocks;
+    f32x4 acc[CT] = {};
+    using AGroup = std::conditional_t<A_MX, MxGroup, Bf16Group>;
+    auto load_a = [&](int c, int g, auto partial) -> AGroup {
+        constexpr bool TAIL = decltype(partial)::value;
+        const int64_t arow = min(c * 16 + r, M - 1);
         if constexpr (A_MX) {
-            MxGroup a[CT];
-#pragma unroll
-            for (int c = 0; c < CT; c++)
-                a[c] = load_mx_group(acodes + arow[c] * kbytes, ascales + arow[c] * kb, g, lg, nblk);
+            const uint8_t *ac = acodes + arow * (K / 2), *as = ascales + arow * kb;
+            return TAIL ? load_mx_tail(ac, as, g, lg, tail) : load_mx_group(ac, as, g, lg);
+        } else {
+            const __bf16 *ar = A + arow * lda;
+            return TAIL ? load_bf16_tail(ar, g, lg, tail) : load_bf16_group(ar, g, lg);
+        }
+    };
+    auto product = [&](const MxGroup &w, const AGroup &a, f32x4 &s) {
+        if constexpr (A_MX) {
 #pragma unroll
             for (int i = 0; i < kGroupChunks; i++)
-#pragma unroll
-                for (int t = 0; t < RT; t++)
-#pragma unroll
-                    for (int c = 0; c < CT; c++)
-                        acc[t][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            fp4_operand(w[t].c[i]), fp4_operand(a[c].c[i]), acc[t][c], 4, 4, 0,
-                            (int)(w[t].s[i] >> (8 * lg)), 0, (int)(a[c].s[i] >> (8 * lg)));
+                s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    fp4_operand(w.c[i]), fp4_operand(a.c[i]), s, 4, 4, 0, (int)(w.s[i] >> (8 * lg)), 0,
+                    (int)(a.s[i] >> (8 * lg)));
         } else {
+            group_product(w, a, lg, s);
+        }
+    };
+    if (wave < full) {
+        MxGroup w = load_mx_group(wc, ws, wave, lg);
+        for (int g = wave; g < full; g += waves) {
+            // loads return in order: the activations, which come from L2, go ahead of the next W group
+            const AGroup a = load_a(0, g, std::false_type{});
+            __builtin_amdgcn_sched_barrier(0);
+            const MxGroup next = load_mx_group(wc, ws, min(g + waves, full - 1), lg);
+            __builtin_amdgcn_sched_barrier(0);
+            product(w, a, acc[0]);
 #pragma unroll
-            for (int i = 0; i < kGroupChunks; i++) {
-                const bool ok = i * 4 + lg < nblk;
-                bf16x8 a[CT][4];
-#pragma unroll
-                for (int c = 0; c < CT; c++)
-                    load_bf16_block(A + arow[c] * lda, g * kGroupBlocks + i * 4 + lg, ok, a[c]);
-#pragma unroll
-                for (int t = 0; t < RT; t++) {
-                    const float s = e8m0_to_f32((w[t].s[i] >> (8 * lg)) & 255u);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const bf16x8 wf = fp4_to_bf16x8(w[t].c[i][j], s);
-#pragma unroll
-                        for (int c = 0; c < CT; c++) acc[t][c] = mfma_bf16(wf, a[c][j], acc[t][c]);
-                    }
-                }
-            }
+            for (int c = 1; c < CT; c++) product(w, load_a(c, g, std::false_type{}), acc[c]);
+            w = next;
         }
     }
+    if (tail > 0 && full % waves == wave) {
+        const MxGroup w = load_mx_tail(wc, ws, full, lg, tail);
 #pragma unroll
-    for (int t = 0; t < RT; t++)
+        for (int c = 0; c < CT; c++) product(w, load_a(c, full, std::true_type{}), acc[c]);
+    }
 #pragma unroll
-        for (int c = 0; c < CT; c++)
-            *reinterpret_cast<f32x4 *>(&red[((wave * RT + t) * CT + c) * 256 + lane * 4]) = acc[t][c];
+    for (int c = 0; c < CT; c++)
+        *reinterpret_cast<f32x4 *>(&red[(wave * CT + c) * 256 + lane * 4]) = acc[c];
     __syncthreads();
-    // element (row nl of the tile, column m) sits in lane m % 16 + 16 (nl % 16 / 4), register nl % 4
-    for (int o = threadIdx.x; o < RT * CT * 256; o += blockDim.x) {
-        const int nl = o % (16 * RT), m = o / (16 * RT);
+    // element (row nl of the tile, column m) sits in lane m % 16 + 16 (nl / 4), register nl % 4
+    for (int o = threadIdx.x; o < CT * 256; o += blockDim.x) {
+        const int nl = o % 16, m = o / 16;
         if (m >= M || n0 + nl >= N) continue;
-        const int at = ((nl / 16) * CT + m / 16) * 256 + (m % 16 + 16 * (nl % 16 / 4)) * 4 + nl % 4;
+        const int at = (m / 16) * 256 + (m % 16 + 16 * (nl / 4)) * 4 + nl % 4;
         float s = 0.0f;
-        for (int v = 0; v < waves; v++) s += red[v * (RT * CT * 256) + at];
+        for (int v = 0; v < waves; v++) s += red[v * (CT * 256) + at];
         store_out(C + (int64_t)m * ldc + n0 + nl, s);
     }
 }
@@ -640,32 +624,26 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
     }
 }
 
-template <int CT, int RT, bool A_MX, class OT>
+template <int CT, bool A_MX, class OT>
 void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
                      int64_t ldc, int num_cus, hipStream_t stream) {
     const int64_t N = w->rows, K = w->cols;
-    const int64_t wgs = (N + 16 * RT - 1) / (16 * RT), groups = (K + kGroup - 1) / kGroup;
+    const int64_t wgs = (N + 15) / 16, groups = (K + kGroup - 1) / kGroup;
     // enough waves to keep about 12 per CU streaming, no more than there are groups to share out
     int waves = 4;
     if (wgs * waves < 12 * (int64_t)num_cus) waves = 8;
     while (waves > 1 && waves / 2 >= groups) waves /= 2;
-    const size_t lds = (size_t)waves * RT * CT * 1024;
-    hipLaunchKernelGGL((k_mx_skinny<CT, RT, A_MX, OT>), dim3((unsigned)wgs), dim3(64 * waves), lds, stream,
-                       reinterpret_cast<const __bf16 *>(a_bf16), lda, A_MX ? a_q->codes : nullptr,
-                       A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, N, K, c, ldc);
+    hipLaunchKernelGGL((k_mx_skinny<CT, A_MX, OT>), dim3((unsigned)wgs), dim3(64 * waves), (size_t)waves * CT * 1024,
+                       stream, reinterpret_cast<const __bf16 *>(a_bf16), lda, A_MX ? a_q->codes : nullptr,
+                       A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, N, (int)K, c, ldc);
 }
 
-template <class OT>
+template <bool A_MX, class OT>
 void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
                    int64_t ldc, int num_cus, hipStream_t stream) {
-    const int ct = (int)((M + 15) / 16);
-#define MX_SKINNY(CT)                                                                                        \
-    (a_q ? launch_skinny_t<CT, 1, true, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream)                 \
-         : launch_skinny_t<CT, 1, false, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream))
-    if (ct == 1) MX_SKINNY(1);
-    else if (ct == 2) MX_SKINNY(2);
-    else MX_SKINNY(4);
-#undef MX_SKINNY
+    if (M <= 16) launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+    else if (M <= 32) launch_skinny_t<2, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+    else launch_skinny_t<4, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
 }
 
 template <class OT>
@@ -676,7 +654,8 @@ hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t
         const int64_t blocks = std::min<int64_t>((M * w->rows + 255) / 256, 4096);
         hipLaunchKernelGGL(k_mx_zero<OT>, dim3((unsigned)blocks), dim3(256), 0, stream, c, M, w->rows, ldc);
     } else if (M <= kSkinnyMaxM) {
-        launch_skinny(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        if (a_q) launch_skinny<true>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        else launch_skinny<false>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
     } else {
         launch_tiled(a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     }

@@ -3,21 +3,24 @@
 //
 // Bound by streaming the chosen experts' weights (17/32 byte per element) once from HBM; everything else
 // is small.  Weights go from memory to registers in the matrix instructions' operand layout (MxGroup),
-// are expanded exactly to bf16 (half an instruction per element) and multiply 16 tokens at a time with
-// v_mfma_f32_16x16x32_bf16.
+// are expanded exactly to bf16 (half an instruction per element) and multiply up to 16 tokens at a time with
+// v_mfma_f32_16x16x32_bf16.  Each wave has the weights of its next group in flight while it works on one.
 //
 // Routing needs no kernel of its own: an expert's rank in a row is the number of entries ahead of it
 // (larger, or equal with a lower index), so a workgroup of the first kernel finds which tokens chose its
 // expert by counting, and one further workgroup per token writes that token's choices and softmax sum.
-//   k_moe_up:   workgroup (slot, 16 intermediate rows): gate and up products of the slot's expert for
-//               the tokens that chose it, h = silu(g) u exp(logit - row max), stored as two bf16 planes
-//               (2^-17 of its value) per (token, choice).  With tokens * top_k < experts a slot is a
-//               (token, choice) pair, and the workgroups of a pair whose expert an earlier token chose
-//               leave; otherwise a slot is an expert.
-//   k_moe_down: workgroup (16 rows of Wd): all chosen experts, (expert, 512-column group) items dealt to
-//               the waves; the accumulators run over experts, since h carries the softmax weight; the
-//               row's softmax sum divides at the end.  No atomics: sums are joined in wave order.
+//   k_moe_up:   workgroup (slot, a run of 16-row tiles of the intermediate size): gate and up products of
+//               the slot's expert for the tokens that chose it, h = silu(g) u exp(logit - row max), stored
+//               as two bf16 planes (2^-17 of its value) per (token, choice).  With tokens * top_k <
+//               experts a slot is a (token, choice) pair, and a pair whose expert an earlier token chose
+//               is left empty; otherwise a slot is an expert.  The first run of a slot lists its tokens.
+//   k_moe_down: workgroup (16 rows of Wd): (slot, 512-column group) items dealt to the waves.  h carries the
+//               softmax weight, so a wave adds its items into its own [token][16 rows] sums in LDS; these are
+//               joined in wave order and divided by the softmax sum.  No atomics: the result does not
+//               depend on the order of execution.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "mx.h"
@@ -26,7 +29,7 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kMaxT = MXFP4_MOE_MAX_TOKENS, kMaxE = MXFP4_MOE_MAX_EXPERTS, kMaxK = MXFP4_MOE_MAX_TOP_K;
+constexpr int kMaxT = MXFP4_MOE_MAX_TOKENS, kMaxE = MXFP4_MOE_MAX_EXPERTS;
 constexpr int kUpWaves = 4, kDownWaves = 8;
 
 struct MoeDev {
@@ -34,313 +37,392 @@ struct MoeDev {
     const void *logits;
     int64_t ld_x, ld_logits;
     const uint8_t *gu_codes, *gu_scales, *dn_codes, *dn_scales;
-    int64_t H, I;
+    int H, I;
     void *y;
     int64_t ld_y;
-    int32_t *ids;       // user's, may be null
-    float *weights;     // user's, may be null
-    int32_t *ws_ids;    // [T][k]
-    float *ws_den;      // [T] softmax sum; NaN for a row with NaN or +inf
-    __bf16 *h_hi, *h_lo;  // [T * k][I]
-    int T, E, k, renorm, slots, pair_slots, tiles;
+    int32_t *ids;    // user's, may be null
+    float *weights;  // user's, may be null
+    // workspace
+    float *den;          // [T] softmax sum; NaN for a row with NaN or +inf
+    int32_t *slot_n;     // [slots] tokens of the slot | expert << 16
+    uint16_t *slot_tok;  // [slots][T] token | choice << 8
+    __bf16 *h;           // [T * k][2][I]: the two planes of a (token, choice)
+    int T, E, k, renorm, slots, pair_slots, tiles, tile_run, runs;
 };
 
-template <bool BF16>
-__device__ __forceinline__ float load_logit(const MoeDev &a, int t, int e) {
-    if constexpr (BF16) return (float)reinterpret_cast<const __bf16 *>(a.logits)[(int64_t)t * a.ld_logits + e];
-    else return reinterpret_cast<const float *>(a.logits)[(int64_t)t * a.ld_logits + e];
+// Order of fp32 values as unsigned keys (-0 counts as +0); NaN lies beyond the infinities.
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t u = f2u(v + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_to_f32(uint32_t k) { return u2f(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu, kKeyPosInf = 0xFF800000u;
+
+// A row of logits as keys, one wave: lane l holds entries c * 64 + l.  Entries past E and masked ones are
+// kKeyNegInf.
+template <int EC>
+struct RowKeys {
+    uint32_t k[EC];
+};
+
+template <bool BF16, int EC>
+__device__ __forceinline__ RowKeys<EC> load_row(const MoeDev &a, int t, int lane) {
+    RowKeys<EC> r;
+#pragma unroll
+    for (int c = 0; c < EC; c++) {
+        const int j = c * 64 + lane;
+        const int64_t at = (int64_t)t * a.ld_logits + min(j, a.E - 1);
+        float v;
+        if constexpr (BF16) v = (float)reinterpret_cast<const __bf16 *>(a.logits)[at];
+        else v = reinterpret_cast<const float *>(a.logits)[at];
+        r.k[c] = j < a.E ? key_of(v) : kKeyNegInf;
+    }
+    return r;
+}
+
+// Whether a row holds a NaN or +infinity (a NaN's key is above +infinity's or below -infinity's).
+template <int EC>
+__device__ __forceinline__ bool row_bad(const RowKeys<EC> &r) {
+    bool b = false;
+#pragma unroll
+    for (int c = 0; c < EC; c++) b = b || r.k[c] >= kKeyPosInf || r.k[c] < kKeyNegInf;
+    return __ballot(b) != 0;
+}
+
+template <int EC>
+__device__ __forceinline__ uint32_t row_max(const RowKeys<EC> &r) {
+    uint32_t m = r.k[0];
+#pragma unroll
+    for (int c = 1; c < EC; c++) m = max(m, r.k[c]);
+    return wave_max_u32(m);
+}
+
+// Entry e of the row.
+template <int EC>
+__device__ __forceinline__ uint32_t row_at(const RowKeys<EC> &r, int e) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int c = 0; c < EC; c++)
+        if (e / 64 == c) v = readlane_u32(r.k[c], e % 64);
+    return v;
+}
+
+// Takes the largest entry out of the row (ties: the lowest index); its index, or -1 when none is left.
+template <int EC>
+__device__ __forceinline__ int pop_max(RowKeys<EC> &r, int lane, uint32_t &key) {
+    key = row_max(r);
+    if (key == kKeyNegInf) return -1;
+    int e = -1;
+#pragma unroll
+    for (int c = 0; c < EC; c++) {
+        const uint64_t m = __ballot(r.k[c] == key);
+        if (e < 0 && m != 0) {
+            const int l = __builtin_ctzll(m);
+            e = c * 64 + l;
+            if (lane == l) r.k[c] = kKeyNegInf;
+        }
+    }
+    return e;
+}
+
+// Number of entries ahead of entry e, whose key is ke.
+template <int EC>
+__device__ __forceinline__ int rank_of(const RowKeys<EC> &r, int e, uint32_t ke, int lane) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < EC; c++)
+        n += __popcll(__ballot(r.k[c] > ke || (r.k[c] == ke && c * 64 + lane < e)));
+    return n;
+}
+
+// One token's choices, weights and softmax sum (one wave).
+template <bool BF16, int EC>
+__device__ __forceinline__ void route_token(const MoeDev &a, int t, int lane) {
+    RowKeys<EC> r = load_row<BF16, EC>(a, t, lane);
+    const bool bad = row_bad(r);
+    const uint32_t top = row_max(r);
+    const float ftop = key_to_f32(top);
+    float s = 0.0f;
+    if (!a.renorm) {
+#pragma unroll
+        for (int c = 0; c < EC; c++) s += r.k[c] > kKeyNegInf ? expf(key_to_f32(r.k[c]) - ftop) : 0.0f;
+    }
+    int id = -1;     // lane j < k holds choice j
+    float p = 0.0f;
+    for (int j = 0; j < a.k && !bad; j++) {
+        uint32_t key;
+        const int e = pop_max(r, lane, key);
+        if (e < 0) break;
+        if (lane == j) {
+            id = e;
+            p = expf(key_to_f32(key) - ftop);
+        }
+    }
+    const float den = wave_sum_f32(a.renorm ? p : s);
+    if (lane == 0) a.den[t] = bad ? __builtin_nanf("") : top == kKeyNegInf ? 0.0f : den;
+    if (lane < a.k) {
+        if (a.ids) a.ids[t * a.k + lane] = id;
+        if (a.weights) a.weights[t * a.k + lane] = id >= 0 ? p / den : 0.0f;
+    }
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-__device__ __forceinline__ bool is_bad(float v) { return !(v < __builtin_inff()); }  // NaN or +inf
-
-__device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
-}
-
-// Rank of expert e in row t (one wave, every lane gets the result), the row maximum, and whether the row
-// holds a NaN or +inf.
-template <bool BF16>
-__device__ __forceinline__ int wave_rank(const MoeDev &a, int t, int e, int lane, float &le, float &top, bool &bad) {
-    le = load_logit<BF16>(a, t, e);
-    int n = 0;
-    bool b = false;
-    float m = -__builtin_inff();
-    for (int j = lane; j < a.E; j += 64) {
-        const float v = load_logit<BF16>(a, t, j);
-        b = b || is_bad(v);
-        m = fmaxf(m, v);
-        n += (v > le || (v == le && j < e)) ? 1 : 0;
-    }
-    top = wave_max_f32(m);
-    bad = __any(b);
-    return (int)wave_sum_u32((uint32_t)n);
-}
-
-// One token's choices and softmax sum (a whole workgroup of 256).
-template <bool BF16>
-__device__ void route_token(const MoeDev &a, int t, float *row, int32_t *ids) {
-    __shared__ float sh_top[4], sh_sum[4];
-    __shared__ int sh_bad;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (tid == 0) sh_bad = 0;
-    for (int j = tid; j < a.k; j += 256) ids[j] = -1;
-    __syncthreads();
-    float m = -__builtin_inff();
-    bool b = false;
-    for (int j = tid; j < a.E; j += 256) {
-        const float v = load_logit<BF16>(a, t, j);
-        row[j] = v;
-        b = b || is_bad(v);
-        m = fmaxf(m, v);
-    }
-    m = wave_max_f32(m);
-    if (lane == 0) sh_top[wave] = m;
-    if (b) sh_bad = 1;
-    __syncthreads();
-    const float top = fmaxf(fmaxf(sh_top[0], sh_top[1]), fmaxf(sh_top[2], sh_top[3]));
-    const bool bad = sh_bad != 0;
-    float s = 0.0f;
-    if (!bad) {
-        for (int j = tid; j < a.E; j += 256) {
-            const float v = row[j];
-            if (v == -__builtin_inff()) continue;
-            int n = 0;
-            for (int q = 0; q < a.E; q++) n += (row[q] > v || (row[q] == v && q < j)) ? 1 : 0;
-            if (n < a.k) ids[n] = j;
-            if (!a.renorm) s += expf(v - top);
-        }
-    }
-    __syncthreads();
-    if (a.renorm && !bad && tid < a.k && ids[tid] >= 0) s = expf(row[ids[tid]] - top);
-    s = wave_sum_f32(s);
-    if (lane == 0) sh_sum[wave] = s;
-    __syncthreads();
-    const float den = (sh_sum[0] + sh_sum[1]) + (sh_sum[2] + sh_sum[3]);
-    if (tid == 0) a.ws_den[t] = bad ? __builtin_nanf("") : den;
-    if (tid < a.k) {
-        const int e = ids[tid];
-        a.ws_ids[t * a.k + tid] = e;
-        if (a.ids) a.ids[t * a.k + tid] = e;
-        if (a.weights) a.weights[t * a.k + tid] = e >= 0 ? expf(row[e] - top) / den : 0.0f;
-    }
-}
-
-// One 512-column group of 16 W rows against CT column tiles of 16 activation rows given as bf16 rows
-// (arow[c], `planes` planes `plane` elements apart): acc[c] += W . a.  use[c]: whether the lane's row
-// takes part (others multiply by zero); any[c]: whether any lane's does (uniform).
-template <int CT, int PLANES>
-__device__ __forceinline__ void group_product(const MxGroup &w, const __bf16 *const (&arow)[CT], int64_t plane,
-                                              const bool (&use)[CT], const bool (&any)[CT], int64_t g, int lg,
-                                              int64_t nblk, f32x4 (&acc)[CT]) {
-#pragma unroll
-    for (int i = 0; i < kGroupChunks; i++) {
-        const bool ok = i * 4 + lg < nblk;
-        const int64_t blk = g * kGroupBlocks + i * 4 + lg;
-        const float s = e8m0_to_f32((w.s[i] >> (8 * lg)) & 255u);
-        bf16x8 wf[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) wf[j] = fp4_to_bf16x8(w.c[i][j], s);
-#pragma unroll
-        for (int c = 0; c < CT; c++) {
-            if (!any[c]) continue;
-#pragma unroll
-            for (int p = 0; p < PLANES; p++) {
-                u32x4 v[4] = {};
-                if (ok && use[c]) {
-                    const u32x4 *src = reinterpret_cast<const u32x4 *>(arow[c] + p * plane + blk * kMxBlock);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) v[j] = src[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 4; j++) acc[c] = mfma_bf16(wf[j], __builtin_bit_cast(bf16x8, v[j]), acc[c]);
-            }
-        }
-    }
-}
-
-template <bool LBF16>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
-    __shared__ float sh_row[kMaxE];
-    __shared__ int32_t sh_ids[kMaxK];
-    __shared__ int sh_e, sh_n, sh_rank[kMaxT], sh_tok[kMaxT];
+// NC: column tiles of 16 tokens, enough for T.
+template <bool LBF16, int EC, int NC>
+__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2, 4))) void k_moe_up(MoeDev a) {
+    __shared__ int sh_tok[kMaxT], sh_rank[kMaxT];
     __shared__ float sh_p[kMaxT];
-    __shared__ __align__(16) float red[kUpWaves][2][4][256];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if ((int)blockIdx.x >= a.slots * a.tiles) {
-        route_token<LBF16>(a, blockIdx.x - a.slots * a.tiles, sh_row, sh_ids);
+    __shared__ __align__(16) float red[kUpWaves][2][NC][256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if ((int)blockIdx.x < a.T) {
+        if (wave == 0) route_token<LBF16, EC>(a, blockIdx.x, lane);
         return;
     }
-    const int slot = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+    const int block = blockIdx.x - a.T;
+    const int slot = block / a.runs, run = block % a.runs;
     int e = slot, t0 = 0;
-    if (a.pair_slots) {  // the slot's expert: the entry of row t0 with that rank
+    if (a.pair_slots) {  // the slot's expert: choice slot % k of token slot / k
         t0 = slot / a.k;
-        const int want = slot % a.k;
-        if (tid == 0) sh_e = -1;
-        for (int j = tid; j < a.E; j += 64 * kUpWaves) sh_row[j] = load_logit<LBF16>(a, t0, j);
-        __syncthreads();
-        for (int j = tid; j < a.E; j += 64 * kUpWaves) {
-            const float v = sh_row[j];
-            int n = 0;
-            for (int q = 0; q < a.E; q++) n += (sh_row[q] > v || (sh_row[q] == v && q < j)) ? 1 : 0;
-            if (n == want && v > -__builtin_inff()) sh_e = j;
+        RowKeys<EC> r = load_row<LBF16, EC>(a, t0, lane);
+        const bool bad = row_bad(r);
+        uint32_t key;
+        e = -1;
+        for (int j = slot % a.k; j >= 0 && !bad; j--) {
+            e = pop_max(r, lane, key);
+            if (e < 0) break;
         }
-        __syncthreads();
-        e = sh_e;
-        if (e < 0) return;
-    }
-    for (int t = wave; t < a.T; t += kUpWaves) {
-        float le, top;
-        bool bad;
-        const int n = wave_rank<LBF16>(a, t, e, lane, le, top, bad);
-        if (lane == 0) {
-            sh_rank[t] = (bad || le == -__builtin_inff() || n >= a.k) ? -1 : n;
-            sh_p[t] = expf(le - top);
+        if (e < 0) {
+            if (run == 0 && tid == 0) a.slot_n[slot] = 0;
+            return;
         }
     }
-    __syncthreads();
-    if (wave == 0) {  // compact the tokens that chose e, in order
-        const bool in = lane < a.T && sh_rank[lane] >= 0;
-        const uint64_t m = __ballot(in);
-        if (in) sh_tok[__popcll(m & ((1ull << lane) - 1))] = lane;
-        if (lane == 0) sh_n = __popcll(m);
-    }
-    __syncthreads();
-    const int n = sh_n;
-    if (n == 0 || (a.pair_slots && sh_tok[0] != t0)) return;
+    e = __builtin_amdgcn_readfirstlane(e);
 
     const int r = lane & 15, lg = lane >> 4;
-    const int64_t kb = a.H / kMxBlock, row = (int64_t)e * 2 * a.I + tile * 16 + r;
-    const uint8_t *wc[2], *wsc[2];
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        wc[i] = a.gu_codes + (row + i * a.I) * (a.H / 2);
-        wsc[i] = a.gu_scales + (row + i * a.I) * kb;
-    }
-    const __bf16 *xr[4];
-    bool use[4], any[4];
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-        use[c] = c * 16 + r < n;
-        any[c] = c * 16 < n;
-        xr[c] = a.x + (int64_t)sh_tok[use[c] ? c * 16 + r : 0] * a.ld_x;
-    }
-    f32x4 ag[4] = {}, au[4] = {};
-    const int64_t ngrp = (a.H + kGroup - 1) / kGroup;
-    for (int64_t g = wave; g < ngrp; g += kUpWaves) {
-        const int64_t nblk = kb - g * kGroupBlocks;
-        const MxGroup wg = load_mx_group(wc[0], wsc[0], g, lg, nblk);
-        const MxGroup wu = load_mx_group(wc[1], wsc[1], g, lg, nblk);
-        group_product<4, 1>(wg, xr, 0, use, any, g, lg, nblk, ag);
-        group_product<4, 1>(wu, xr, 0, use, any, g, lg, nblk, au);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-        *reinterpret_cast<f32x4 *>(&red[wave][0][c][lane * 4]) = ag[c];
-        *reinterpret_cast<f32x4 *>(&red[wave][1][c][lane * 4]) = au[c];
+    const int kb = a.H / kMxBlock, full = a.H / kGroup, tail = kb - full * kGroupBlocks;
+    const int groups = full + (tail > 0 ? 1 : 0);
+    const int tile0 = run * a.tile_run, ntile = min(a.tile_run, a.tiles - tile0);
+    struct Pair {
+        MxGroup g, u;
+    };
+    // the wave's (tile, group) items, in order: group wave + kUpWaves j of tile 0, 1, ...
+    auto load_w = [&](int tile, int g) -> Pair {
+        const int64_t row = (int64_t)e * 2 * a.I + (tile0 + tile) * 16 + r;
+        const uint8_t *gc = a.gu_codes + row * (a.H / 2), *gs = a.gu_scales + row * kb;
+        const uint8_t *uc = gc + (int64_t)a.I * (a.H / 2), *us = gs + (int64_t)a.I * kb;
+        if (g < full) return Pair{load_mx_group(gc, gs, g, lg), load_mx_group(uc, us, g, lg)};
+        return Pair{load_mx_tail(gc, gs, g, lg, tail), load_mx_tail(uc, us, g, lg, tail)};
+    };
+    Pair w{};
+    if (wave < groups) w = load_w(0, wave);  // in flight while the tokens are looked up
+
+    // the tokens that chose e
+    for (int t = wave; t < a.T; t += kUpWaves) {
+        const RowKeys<EC> row = load_row<LBF16, EC>(a, t, lane);
+        const uint32_t ke = row_at(row, e);
+        const int n = rank_of(row, e, ke, lane);
+        const float top = key_to_f32(row_max(row));
+        if (lane == 0) {
+            sh_rank[t] = row_bad(row) || ke == kKeyNegInf || n >= a.k ? -1 : n;
+            sh_p[t] = expf(key_to_f32(ke) - top);
+        }
     }
     __syncthreads();
-    for (int o = tid; o < n * 16; o += 64 * kUpWaves) {
-        const int il = o % 16, j = o / 16;
-        const int at = (j % 16 + 16 * (il / 4)) * 4 + il % 4;
-        float gs = 0.0f, us = 0.0f;
+    const bool in = lane < a.T && sh_rank[lane] >= 0;  // every wave, the same
+    const uint64_t chosen = __ballot(in);
+    const int n = __popcll(chosen);
+    const bool leader = n > 0 && (!a.pair_slots || __builtin_ctzll(chosen) == t0);
+    const int at = __popcll(chosen & ((1ull << lane) - 1));
+    if (run == 0 && wave == 0) {
+        if (lane == 0) a.slot_n[slot] = leader ? n | e << 16 : 0;
+        if (leader && in) a.slot_tok[slot * a.T + at] = (uint16_t)(lane | sh_rank[lane] << 8);
+    }
+    if (!leader) return;
+    if (in && wave == 0) sh_tok[at] = lane;
+    __syncthreads();
+
+    const int nct = (n + 15) / 16;
+    const __bf16 *xr[NC];
 #pragma unroll
-        for (int w = 0; w < kUpWaves; w++) {
-            gs += red[w][0][j / 16][at];
-            us += red[w][1][j / 16][at];
+    for (int c = 0; c < NC; c++)  // columns past the last token repeat the first; they are not stored
+        xr[c] = a.x + (int64_t)sh_tok[c * 16 + r < n ? c * 16 + r : 0] * a.ld_x;
+    for (int tile = 0; tile < ntile; tile++) {
+        f32x4 ag[NC] = {}, au[NC] = {};
+        for (int g = wave; g < groups; g += kUpWaves) {
+            const bool last = g + kUpWaves >= groups;
+            auto load_x = [&](int c) { return g < full ? load_bf16_group(xr[c], g, lg) : load_bf16_tail(xr[c], g, lg, tail); };
+            // loads return in order: the activations, which come from L2, go ahead of the next weights
+            Bf16Group x = load_x(0);
+            __builtin_amdgcn_sched_barrier(0);
+            const Pair next = load_w(last ? min(tile + 1, ntile - 1) : tile, last ? wave : g + kUpWaves);
+            __builtin_amdgcn_sched_barrier(0);
+            group_product(w.g, x, lg, ag[0]);
+            group_product(w.u, x, lg, au[0]);
+#pragma unroll
+            for (int c = 1; c < NC; c++)
+                if (c < nct) {
+                    x = load_x(c);
+                    group_product(w.g, x, lg, ag[c]);
+                    group_product(w.u, x, lg, au[c]);
+                }
+            w = next;
         }
-        const int t = sh_tok[j];
-        const float h = silu(gs) * us * sh_p[t];
-        const __bf16 hi = (__bf16)h;
-        const int64_t dst = (int64_t)(t * a.k + sh_rank[t]) * a.I + tile * 16 + il;
-        a.h_hi[dst] = hi;
-        a.h_lo[dst] = (__bf16)(h - (float)hi);
+        if (tile > 0) __syncthreads();  // the previous tile's sums have been read
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+            if (c < nct) {
+                *reinterpret_cast<f32x4 *>(&red[wave][0][c][lane * 4]) = ag[c];
+                *reinterpret_cast<f32x4 *>(&red[wave][1][c][lane * 4]) = au[c];
+            }
+        __syncthreads();
+        // element (row il of the tile, column j) sits in lane j % 16 + 16 (il / 4), register il % 4
+        for (int o = tid; o < n * 16; o += 64 * kUpWaves) {
+            const int il = o % 16, j = o / 16;
+            const int src = (j % 16 + 16 * (il / 4)) * 4 + il % 4;
+            float gs = 0.0f, us = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kUpWaves; v++) {
+                gs += red[v][0][j / 16][src];
+                us += red[v][1][j / 16][src];
+            }
+            const int t = sh_tok[j];
+            const float h = silu(gs) * us * sh_p[t];
+            const __bf16 hi = (__bf16)h;
+            __bf16 *dst = a.h + (int64_t)(t * a.k + sh_rank[t]) * 2 * a.I + (tile0 + tile) * 16 + il;
+            dst[0] = hi;
+            dst[a.I] = (__bf16)(h - (float)hi);
+        }
     }
 }
+
+// Eight tokens at a time: columns 0-7 of the matrix instruction take the high planes of their h, columns 8-15
+// the low planes, and the two halves of the result are added.
+constexpr int kDownTokens = 8;
 
 template <class OT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
-    __shared__ int sh_ids[kMaxT * kMaxK];
-    __shared__ int sh_used[kMaxE], sh_list[kMaxE], sh_nd;
-    __shared__ __align__(16) float red[kDownWaves][4][256];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int pairs = a.T * a.k;
-    for (int j = tid; j < a.E; j += 64 * kDownWaves) sh_used[j] = 0;
+    extern __shared__ __align__(16) float sums[];  // [waves][T][16]
+    __shared__ int sh_list[kMaxE], sh_info[kMaxE], sh_cnt[kDownWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    static_assert(kMaxE <= 64 * kDownWaves, "one thread per slot");
+    // the slots with tokens, in order
+    const int info = tid < a.slots ? a.slot_n[tid] : 0;
+    const uint64_t m = __ballot(info != 0);
+    if (lane == 0) sh_cnt[wave] = __popcll(m);
+    float *mine = sums + wave * a.T * 16;
+    for (int j = lane; j < a.T * 16; j += 64) mine[j] = 0.0f;
     __syncthreads();
-    for (int j = tid; j < pairs; j += 64 * kDownWaves) {
-        const int e = a.ws_ids[j];
-        sh_ids[j] = e;
-        if (e >= 0) sh_used[e] = 1;
-    }
-    __syncthreads();
-    if (wave == 0) {  // the distinct experts, ascending
-        int base = 0;
-        for (int j0 = 0; j0 < a.E; j0 += 64) {
-            const bool in = j0 + lane < a.E && sh_used[j0 + lane] != 0;
-            const uint64_t m = __ballot(in);
-            if (in) sh_list[base + __popcll(m & ((1ull << lane) - 1))] = j0 + lane;
-            base += __popcll(m);
-        }
-        if (lane == 0) sh_nd = base;
-    }
-    __syncthreads();
-    const int r = lane & 15, lg = lane >> 4;
-    const int64_t kb = a.I / kMxBlock, n0 = (int64_t)blockIdx.x * 16;
-    const int64_t ngrp = (a.I + kGroup - 1) / kGroup, items = sh_nd * ngrp;
-    const int64_t plane = a.h_lo - a.h_hi;
-    f32x4 acc[4] = {};
-    for (int64_t it = wave; it < items; it += kDownWaves) {
-        const int e = sh_list[it / ngrp];
-        const int64_t g = it % ngrp, nblk = kb - g * kGroupBlocks;
-        const int64_t row = (int64_t)e * a.H + n0 + r;
-        const MxGroup w = load_mx_group(a.dn_codes + row * (a.I / 2), a.dn_scales + row * kb, g, lg, nblk);
-        const __bf16 *hr[4];
-        bool use[4], any[4];
+    int base = 0, total = 0;
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-            const int t = c * 16 + r;
-            int at = -1;
-            if (t < a.T)
-                for (int q = 0; q < a.k; q++)
-                    if (sh_ids[t * a.k + q] == e) at = t * a.k + q;
-            use[c] = at >= 0;
-            any[c] = __any(use[c]);
-            hr[c] = a.h_hi + (int64_t)(use[c] ? at : 0) * a.I;
-        }
-        group_product<4, 2>(w, hr, plane, use, any, g, lg, nblk, acc);
+    for (int v = 0; v < kDownWaves; v++) {
+        if (v < wave) base += sh_cnt[v];
+        total += sh_cnt[v];
     }
+    if (info != 0) {
+        const int at = base + __popcll(m & ((1ull << lane) - 1));
+        sh_list[at] = tid;
+        sh_info[at] = info;
+    }
+    __syncthreads();
+    total = __builtin_amdgcn_readfirstlane(total);
+
+    const int r = lane & 15, lg = lane >> 4, plane = r / kDownTokens;
+    const int kb = a.I / kMxBlock, full = a.I / kGroup, tail = kb - full * kGroupBlocks;
+    const int groups = full + (tail > 0 ? 1 : 0), items = total * groups;
+    const int n0 = blockIdx.x * 16;
+    auto load_w = [&](int it) -> MxGroup {
+        const int g = it % groups;
+        const int64_t row = (int64_t)(sh_info[it / groups] >> 16) * a.H + n0 + r;
+        const uint8_t *c = a.dn_codes + row * (a.I / 2), *s = a.dn_scales + row * kb;
+        return g < full ? load_mx_group(c, s, g, lg) : load_mx_tail(c, s, g, lg, tail);
+    };
+    // the lane's token (and choice) in pass q of an item's tokens
+    auto load_tok = [&](int it, int q) -> int {
+        const int at = it / groups, n = sh_info[at] & 0xFFFF, j = q * kDownTokens + r % kDownTokens;
+        return a.slot_tok[sh_list[at] * a.T + (j < n ? j : 0)];
+    };
+    MxGroup w{};
+    int tok = 0;
+    if (wave < items) {
+        tok = load_tok(wave, 0);
+        w = load_w(wave);
+    }
+    for (int it = wave; it < items; it += kDownWaves) {
+        const int g = it % groups, n = __builtin_amdgcn_readfirstlane(sh_info[it / groups] & 0xFFFF);
+        const int passes = (n + kDownTokens - 1) / kDownTokens, nx = min(it + kDownWaves, items - 1);
+        MxGroup next;
+        int next_tok;
+        for (int q = 0; q < passes; q++) {
+            const __bf16 *row = a.h + ((int64_t)((tok & 255) * a.k + (tok >> 8)) * 2 + plane) * a.I;
+            const Bf16Group h = g < full ? load_bf16_group(row, g, lg) : load_bf16_tail(row, g, lg, tail);
+            __builtin_amdgcn_sched_barrier(0);
+            // loads return in order: what the next pass or item needs goes behind
+            const int t = tok & 255;
+            if (q + 1 < passes) {
+                tok = load_tok(it, q + 1);
+            } else {
+                next_tok = load_tok(nx, 0);
+                next = load_w(nx);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 acc = {};
+            group_product(w, h, lg, acc);
+            // columns c and c + 8 of a row of 16 lanes
 #pragma unroll
-    for (int c = 0; c < 4; c++) *reinterpret_cast<f32x4 *>(&red[wave][c][lane * 4]) = acc[c];
+            for (int i = 0; i < 4; i++) {
+                const float v = acc[i];
+                acc[i] = v + u2f(dpp_u32<kDppRowRor8>(f2u(v)));
+            }
+            if (r < kDownTokens && q * kDownTokens + r < n) {
+                f32x4 *dst = reinterpret_cast<f32x4 *>(&mine[t * 16 + lg * 4]);
+                f32x4 s = *dst;
+                s += acc;
+                *dst = s;
+            }
+        }
+        w = next;
+        tok = next_tok;
+    }
     __syncthreads();
     OT *y = reinterpret_cast<OT *>(a.y);
     for (int o = tid; o < a.T * 16; o += 64 * kDownWaves) {
-        const int nl = o % 16, t = o / 16;
-        const int at = (t % 16 + 16 * (nl / 4)) * 4 + nl % 4;
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWaves; w++) s += red[w][t / 16][at];
-        const float den = a.ws_den[t];
+        for (int v = 0; v < kDownWaves; v++) s += sums[v * a.T * 16 + o];
+        const int t = o / 16;
+        const float den = a.den[t];
         // no expert: 0; a row with NaN or +inf has den = NaN
-        const float v = den == 0.0f ? 0.0f : s / den;
-        y[(int64_t)t * a.ld_y + n0 + nl] = (OT)v;
+        y[(int64_t)t * a.ld_y + n0 + o % 16] = (OT)(den == 0.0f ? 0.0f : s / den);
     }
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
+template <bool LBF16, int NC>
+void launch_up_e(const MoeDev &a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.T + a.slots * a.runs)), block(64 * kUpWaves);
+    if (a.E <= 64) hipLaunchKernelGGL((k_moe_up<LBF16, 1, NC>), grid, block, 0, stream, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((k_moe_up<LBF16, 2, NC>), grid, block, 0, stream, a);
+    else if (a.E <= 256) hipLaunchKernelGGL((k_moe_up<LBF16, 4, NC>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((k_moe_up<LBF16, 8, NC>), grid, block, 0, stream, a);
+}
+
+template <bool LBF16>
+void launch_up(const MoeDev &a, hipStream_t stream) {
+    if (a.T <= 16) launch_up_e<LBF16, 1>(a, stream);
+    else launch_up_e<LBF16, 4>(a, stream);
+}
+
 }  // namespace
 
 size_t mx_moe_ws_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
     if (tokens <= 0 || top_k <= 0 || inter < 0) return 0;
-    return align256((size_t)tokens * top_k * 4) + align256((size_t)tokens * 4) +
-           2 * align256((size_t)tokens * top_k * inter * 2);
+    return align256(kMaxT * 4) + align256(kMaxE * 4) + align256((size_t)kMaxE * tokens * 2) +
+           align256((size_t)tokens * top_k * inter * 4);
 }
 
 hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStream_t stream) {
-    (void)num_cus;
     MoeDev a{};
     a.x = reinterpret_cast<const __bf16 *>(p.x);
     a.logits = p.logits;
@@ -350,8 +432,8 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     a.gu_scales = p.w_gate_up->scales;
     a.dn_codes = p.w_down->codes;
     a.dn_scales = p.w_down->scales;
-    a.H = p.w_gate_up->cols;
-    a.I = p.w_down->cols;
+    a.H = (int)p.w_gate_up->cols;
+    a.I = (int)p.w_down->cols;
     a.y = p.y;
     a.ld_y = p.ld_y;
     a.ids = p.ids;
@@ -361,20 +443,25 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     a.k = p.top_k;
     a.renorm = p.renormalize;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
-    a.ws_ids = reinterpret_cast<int32_t *>(ws);
-    ws += align256((size_t)a.T * a.k * 4);
-    a.ws_den = reinterpret_cast<float *>(ws);
-    ws += align256((size_t)a.T * 4);
-    a.h_hi = reinterpret_cast<__bf16 *>(ws);
-    a.h_lo = reinterpret_cast<__bf16 *>(ws + align256((size_t)a.T * a.k * a.I * 2));
+    a.den = reinterpret_cast<float *>(ws);
+    ws += align256(kMaxT * 4);
+    a.slot_n = reinterpret_cast<int32_t *>(ws);
+    ws += align256(kMaxE * 4);
+    a.slot_tok = reinterpret_cast<uint16_t *>(ws);
+    ws += align256((size_t)kMaxE * a.T * 2);
+    a.h = reinterpret_cast<__bf16 *>(ws);
     a.pair_slots = a.T * a.k < a.E ? 1 : 0;
     a.slots = a.pair_slots ? a.T * a.k : a.E;
-    a.tiles = (int)(a.I / 16);
-    const dim3 up((unsigned)(a.slots * a.tiles + a.T)), down((unsigned)(a.H / 16));
-    if (p.logits_bf16) hipLaunchKernelGGL(k_moe_up<true>, up, dim3(64 * kUpWaves), 0, stream, a);
-    else hipLaunchKernelGGL(k_moe_up<false>, up, dim3(64 * kUpWaves), 0, stream, a);
-    if (p.y_bf16) hipLaunchKernelGGL(k_moe_down<__bf16>, down, dim3(64 * kDownWaves), 0, stream, a);
-    else hipLaunchKernelGGL(k_moe_down<float>, down, dim3(64 * kDownWaves), 0, stream, a);
+    a.tiles = a.I / 16;
+    // tiles per workgroup: several where the slots give the device more than eight workgroups per CU
+    a.tile_run = std::min(8, std::max(1, (int)((int64_t)a.slots * a.tiles / (8 * num_cus))));
+    a.runs = (a.tiles + a.tile_run - 1) / a.tile_run;
+    if (p.logits_bf16) launch_up<true>(a, stream);
+    else launch_up<false>(a, stream);
+    const dim3 down((unsigned)(a.H / 16));
+    const size_t lds = (size_t)kDownWaves * a.T * 16 * 4;
+    if (p.y_bf16) hipLaunchKernelGGL(k_moe_down<__bf16>, down, dim3(64 * kDownWaves), lds, stream, a);
+    else hipLaunchKernelGGL(k_moe_down<float>, down, dim3(64 * kDownWaves), lds, stream, a);
     return hipGetLastError();
 }
 
