@@ -70,8 +70,8 @@ __device__ __forceinline__ MxGroup load_mx_tail(const uint8_t *codes, const uint
     return r;
 }
 
-// Eight codes -> eight bf16 values e2m1 x 2^(b - 127), exact (the scaled conversion applies the exponent
-// of `scale`).
+// Eight codes -> eight bf16 values e2m1 x 2^(b - 127), exact.  The scaled conversion reads only the exponent
+// field of `scale`, as E8M0: 0 is 2^-127 and 255 NaN; its sign and mantissa do not matter.
 __device__ __forceinline__ bf16x8 fp4_to_bf16x8(uint32_t w, float scale) {
     bf16x2 p[4];
     p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
@@ -79,6 +79,11 @@ __device__ __forceinline__ bf16x8 fp4_to_bf16x8(uint32_t w, float scale) {
     p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
     p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
     return bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+}
+
+// Byte `lg` of a word of scale bytes in the exponent field of a conversion scale.
+__device__ __forceinline__ float scale_operand(uint32_t word, int lg) {
+    return u2f(__builtin_rotateright32(word, 8 * lg + 9));
 }
 
 __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -90,38 +95,37 @@ struct Bf16Group {
     u32x4 v[kGroupChunks][4];
 };
 
-__device__ __forceinline__ Bf16Group load_bf16_group(const __bf16 *row, int grp, int lg) {
-    Bf16Group r;
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (int64_t)grp * kGroup + lg * kMxBlock);
-#pragma unroll
-    for (int i = 0; i < kGroupChunks; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) r.v[i][j] = p[i * 16 + j];
-    return r;
-}
-
-__device__ __forceinline__ Bf16Group load_bf16_tail(const __bf16 *row, int grp, int lg, int nblk) {
+// nblk: blocks of the row from the start of the group on; those past the end read as zero.
+template <bool TAIL>
+__device__ __forceinline__ Bf16Group load_bf16_group(const __bf16 *row, int grp, int lg, int nblk = kGroupBlocks) {
     Bf16Group r;
     const u32x4 *p = reinterpret_cast<const u32x4 *>(row + (int64_t)grp * kGroup + lg * kMxBlock);
 #pragma unroll
     for (int i = 0; i < kGroupChunks; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            r.v[i][j] = u32x4{0, 0, 0, 0};
-            if (i * 4 + lg < nblk) r.v[i][j] = p[i * 16 + j];
+            if constexpr (TAIL) {
+                r.v[i][j] = u32x4{0, 0, 0, 0};
+                if (i * 4 + lg < nblk) r.v[i][j] = p[i * 16 + j];
+            } else {
+                r.v[i][j] = p[i * 16 + j];
+            }
         }
     return r;
 }
 
-// acc += W . a over a group: the lane's W blocks are expanded exactly to bf16, sixteen instructions.
-__device__ __forceinline__ void group_product(const MxGroup &w, const Bf16Group &a, int lg, f32x4 &acc) {
+// acc[t] += W[t] . a over a group: the lane's W blocks are expanded exactly to bf16, sixteen instructions a tile.
+template <int RT>
+__device__ __forceinline__ void group_product(const MxGroup (&w)[RT], const Bf16Group &a, int lg, f32x4 (&acc)[RT]) {
 #pragma unroll
-    for (int i = 0; i < kGroupChunks; i++) {
-        const float s = e8m0_to_f32((w.s[i] >> (8 * lg)) & 255u);
+    for (int i = 0; i < kGroupChunks; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            acc = mfma_bf16(fp4_to_bf16x8(w.c[i][j], s), __builtin_bit_cast(bf16x8, a.v[i][j]), acc);
-    }
+        for (int t = 0; t < RT; t++) {
+            const float s = scale_operand(w[t].s[i], lg);
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                acc[t] = mfma_bf16(fp4_to_bf16x8(w[t].c[i][j], s), __builtin_bit_cast(bf16x8, a.v[i][j]), acc[t]);
+        }
 }
 
 // Host side ---------------------------------------------------------------------------------------

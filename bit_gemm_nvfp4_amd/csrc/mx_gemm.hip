@@ -4,11 +4,11 @@
 // elements of K, which is MXFP4 as stored: codes and scale bytes go from memory to the matrix cores
 // without any expansion.
 //
-// k_mx_skinny (M <= 64): bound by streaming W.  A wave reads 16 W rows straight into registers in the
+// k_mx_skinny (M <= 16): bound by streaming W.  A wave reads 16 W rows straight into registers in the
 //   operand layout (MxGroup), the waves of a workgroup split K and add their partial tiles in LDS in
 //   wave order.  MXFP4 activations take v_mfma_scale_f32_16x16x128; bf16 activations take
 //   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element).
-// k_mx_tile (M > 64): BM x BN output tile per workgroup, operands through LDS by direct-to-LDS loads,
+// k_mx_tile (M > 16): BM x BN output tile per workgroup, operands through LDS by direct-to-LDS loads,
 //   v_mfma_scale_f32_32x32x64 for MXFP4 activations, v_mfma_f32_32x32x16_bf16 for bf16 ones.
 #include <hip/hip_runtime.h>
 
@@ -22,7 +22,7 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kSkinnyMaxM = 64;
+constexpr int kSkinnyMaxM = 16;
 
 template <class OT>
 __device__ __forceinline__ void store_out(OT *p, float v) {
@@ -30,86 +30,95 @@ __device__ __forceinline__ void store_out(OT *p, float v) {
 }
 
 // -------------------------------------------------------------------------------------------------
-// M <= 64
+// M <= 16
 // -------------------------------------------------------------------------------------------------
-// The W groups of a wave are wave, wave + waves, ...; the next one's loads are issued before the current
-// one's products, so two are in flight per wave.
-template <int CT, bool A_MX, class OT>
+// RT tiles of 16 W rows per wave share its activation operands.  The W groups of a wave are wave, wave +
+// waves, ...; the next one's loads are issued before the current one's products.
+template <int RT, bool A_MX, class OT>
 __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A, int64_t lda,
                                                    const uint8_t *__restrict__ acodes,
                                                    const uint8_t *__restrict__ ascales, int M,
                                                    const uint8_t *__restrict__ wcodes,
                                                    const uint8_t *__restrict__ wscales, int64_t N, int K,
                                                    OT *__restrict__ C, int64_t ldc) {
-    extern __shared__ float red[];  // [waves][CT][256]
+    extern __shared__ float red[];  // [waves][RT][256]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int kb = K / kMxBlock;
-    // rows past N (and past M below) repeat the last one; their results are not stored
-    const int64_t row = min(n0 + r, N - 1);
-    const uint8_t *wc = wcodes + row * (K / 2), *ws = wscales + row * kb;
-    const int full = K / kGroup, tail = kb - full * kGroupBlocks;
-    f32x4 acc[CT] = {};
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    const int kb = K / kMxBlock, full = K / kGroup, tail = kb - full * kGroupBlocks;
+    // rows past N or M repeat the last one; their results are not stored
+    const uint8_t *wc[RT], *ws[RT];
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+        const int64_t row = min(n0 + 16 * i + r, N - 1);
+        wc[i] = wcodes + row * (K / 2);
+        ws[i] = wscales + row * kb;
+    }
+    const int64_t arow = min(r, M - 1);
+    const uint8_t *ac = acodes + arow * (K / 2), *as = ascales + arow * kb;
+    const __bf16 *ar = A + arow * lda;
     using AGroup = std::conditional_t<A_MX, MxGroup, Bf16Group>;
-    auto load_a = [&](int c, int g, auto partial) -> AGroup {
-        constexpr bool TAIL = decltype(partial)::value;
-        const int64_t arow = min(c * 16 + r, M - 1);
-        if constexpr (A_MX) {
-            const uint8_t *ac = acodes + arow * (K / 2), *as = ascales + arow * kb;
-            return TAIL ? load_mx_tail(ac, as, g, lg, tail) : load_mx_group(ac, as, g, lg);
-        } else {
-            const __bf16 *ar = A + arow * lda;
-            return TAIL ? load_bf16_tail(ar, g, lg, tail) : load_bf16_group(ar, g, lg);
-        }
-    };
-    auto product = [&](const MxGroup &w, const AGroup &a, f32x4 &s) {
+    f32x4 acc[RT] = {};
+    auto product = [&](const MxGroup (&w)[RT], const AGroup &a) {
         if constexpr (A_MX) {
 #pragma unroll
             for (int i = 0; i < kGroupChunks; i++)
-                s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fp4_operand(w.c[i]), fp4_operand(a.c[i]), s, 4, 4, 0, (int)(w.s[i] >> (8 * lg)), 0,
-                    (int)(a.s[i] >> (8 * lg)));
+#pragma unroll
+                for (int t = 0; t < RT; t++)
+                    acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fp4_operand(w[t].c[i]), fp4_operand(a.c[i]), acc[t], 4, 4, 0, (int)(w[t].s[i] >> (8 * lg)), 0,
+                        (int)(a.s[i] >> (8 * lg)));
         } else {
-            group_product(w, a, lg, s);
+            group_product<RT>(w, a, lg, acc);
         }
     };
+    auto load_a = [&](int g) -> AGroup {
+        if constexpr (A_MX) return load_mx_group(ac, as, g, lg);
+        else return load_bf16_group<false>(ar, g, lg);
+    };
+    MxGroup w[RT];
     if (wave < full) {
-        MxGroup w = load_mx_group(wc, ws, wave, lg);
-        for (int g = wave; g < full; g += waves) {
-            // loads return in order: the activations, which come from L2, go ahead of the next W group
-            const AGroup a = load_a(0, g, std::false_type{});
-            __builtin_amdgcn_sched_barrier(0);
-            const MxGroup next = load_mx_group(wc, ws, min(g + waves, full - 1), lg);
-            __builtin_amdgcn_sched_barrier(0);
-            product(w, a, acc[0]);
 #pragma unroll
-            for (int c = 1; c < CT; c++) product(w, load_a(c, g, std::false_type{}), acc[c]);
-            w = next;
+        for (int i = 0; i < RT; i++) w[i] = load_mx_group(wc[i], ws[i], wave, lg);
+        int g = wave;
+        for (; g + waves < full; g += waves) {
+            // loads return in order: the activations, which come from L2, go ahead of the next W group
+            const AGroup a = load_a(g);
+            __builtin_amdgcn_sched_barrier(0);
+            MxGroup next[RT];
+#pragma unroll
+            for (int i = 0; i < RT; i++) next[i] = load_mx_group(wc[i], ws[i], g + waves, lg);
+            __builtin_amdgcn_sched_barrier(0);
+            product(w, a);
+#pragma unroll
+            for (int i = 0; i < RT; i++) w[i] = next[i];
         }
+        product(w, load_a(g));
     }
     if (tail > 0 && full % waves == wave) {
-        const MxGroup w = load_mx_tail(wc, ws, full, lg, tail);
+        AGroup a;
+        if constexpr (A_MX) a = load_mx_tail(ac, as, full, lg, tail);
+        else a = load_bf16_group<true>(ar, full, lg, tail);
 #pragma unroll
-        for (int c = 0; c < CT; c++) product(w, load_a(c, full, std::true_type{}), acc[c]);
+        for (int i = 0; i < RT; i++) w[i] = load_mx_tail(wc[i], ws[i], full, lg, tail);
+        product(w, a);
     }
 #pragma unroll
-    for (int c = 0; c < CT; c++)
-        *reinterpret_cast<f32x4 *>(&red[(wave * CT + c) * 256 + lane * 4]) = acc[c];
+    for (int i = 0; i < RT; i++) *reinterpret_cast<f32x4 *>(&red[(wave * RT + i) * 256 + lane * 4]) = acc[i];
     __syncthreads();
-    // element (row nl of the tile, column m) sits in lane m % 16 + 16 (nl / 4), register nl % 4
-    for (int o = threadIdx.x; o < CT * 256; o += blockDim.x) {
-        const int nl = o % 16, m = o / 16;
-        if (m >= M || n0 + nl >= N) continue;
-        const int at = (m / 16) * 256 + (m % 16 + 16 * (nl / 4)) * 4 + nl % 4;
+    // element (row nl of the tiles, column m) sits in lane m + 16 (nl % 16 / 4), register nl % 4 of tile nl / 16
+    for (int o = threadIdx.x; o < M * 16 * RT; o += blockDim.x) {
+        const int nl = o % (16 * RT), m = o / (16 * RT);
+        if (n0 + nl >= N) continue;
+        const int at = (nl / 16) * 256 + (m + 16 * (nl % 16 / 4)) * 4 + nl % 4;
         float s = 0.0f;
-        for (int v = 0; v < waves; v++) s += red[v * (CT * 256) + at];
+        for (int v = 0; v < waves; v++) s += red[v * (RT * 256) + at];
         store_out(C + (int64_t)m * ldc + n0 + nl, s);
     }
 }
 
 // -------------------------------------------------------------------------------------------------
-// M > 64
+// M > 16
 // -------------------------------------------------------------------------------------------------
 // One LDS stage holds BK columns of the tile's rows as they are in memory: 128 bytes of an A row (256 MXFP4
 // or 64 bf16 elements) and BK / 2 bytes of a W row, in 16-byte pieces (an MXFP4 block, or 8 bf16 elements).
@@ -394,7 +403,7 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         }
         if constexpr (!T::A_MX) {
 #pragma unroll
-            for (int j = 0; j < T::TN; j++) sf[j] = e8m0_to_f32((uint32_t)sb[j]);
+            for (int j = 0; j < T::TN; j++) sf[j] = scale_operand((uint32_t)sb[j], 0);
         }
         __builtin_amdgcn_sched_barrier(0);
         read_frags(f[1], s, 1);
@@ -624,26 +633,24 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
     }
 }
 
-template <int CT, bool A_MX, class OT>
+template <int RT, bool A_MX, class OT>
 void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
-                     int64_t ldc, int num_cus, hipStream_t stream) {
-    const int64_t N = w->rows, K = w->cols;
-    const int64_t wgs = (N + 15) / 16, groups = (K + kGroup - 1) / kGroup;
-    // enough waves to keep about 12 per CU streaming, no more than there are groups to share out
-    int waves = 4;
-    if (wgs * waves < 12 * (int64_t)num_cus) waves = 8;
-    while (waves > 1 && waves / 2 >= groups) waves /= 2;
-    hipLaunchKernelGGL((k_mx_skinny<CT, A_MX, OT>), dim3((unsigned)wgs), dim3(64 * waves), (size_t)waves * CT * 1024,
-                       stream, reinterpret_cast<const __bf16 *>(a_bf16), lda, A_MX ? a_q->codes : nullptr,
-                       A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, N, (int)K, c, ldc);
+                     int64_t ldc, int waves, hipStream_t stream) {
+    const unsigned wgs = (unsigned)((w->rows + 16 * RT - 1) / (16 * RT));
+    hipLaunchKernelGGL((k_mx_skinny<RT, A_MX, OT>), dim3(wgs), dim3(64 * waves), (size_t)waves * RT * 1024, stream,
+                       reinterpret_cast<const __bf16 *>(a_bf16), lda, A_MX ? a_q->codes : nullptr,
+                       A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, w->rows, (int)w->cols, c, ldc);
 }
 
 template <bool A_MX, class OT>
 void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
                    int64_t ldc, int num_cus, hipStream_t stream) {
-    if (M <= 16) launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
-    else if (M <= 32) launch_skinny_t<2, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
-    else launch_skinny_t<4, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+    const int64_t groups = (w->cols + kGroup - 1) / kGroup;
+    // enough waves to keep about 12 per CU streaming, no more than there are groups to share out
+    int waves = 4;
+    if ((w->rows + 15) / 16 * waves < 12 * (int64_t)num_cus) waves = 8;
+    while (waves > 1 && waves / 2 >= groups) waves /= 2;
+    launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
 }
 
 template <class OT>

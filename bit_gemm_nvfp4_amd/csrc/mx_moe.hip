@@ -30,7 +30,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kMaxT = MXFP4_MOE_MAX_TOKENS, kMaxE = MXFP4_MOE_MAX_EXPERTS;
-constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kUpWaves = 8, kDownWaves = 8;
+constexpr int kUpTiles = 4;  // tiles whose sums a wave keeps before the waves join them
 
 struct MoeDev {
     const __bf16 *x;
@@ -168,12 +169,13 @@ __device__ __forceinline__ void route_token(const MoeDev &a, int t, int lane) {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// NC: column tiles of 16 tokens, enough for T.
-template <bool LBF16, int EC, int NC>
-__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2, 4))) void k_moe_up(MoeDev a) {
+// XREG: H has no more 512-column groups than there are waves, so that a wave's activations are the same for
+// all its tiles and stay in registers.
+template <bool LBF16, int EC, bool XREG>
+__global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
     __shared__ int sh_tok[kMaxT], sh_rank[kMaxT];
     __shared__ float sh_p[kMaxT];
-    __shared__ __align__(16) float red[kUpWaves][2][NC][256];
+    __shared__ __align__(16) float red[kUpWaves][kUpTiles][2][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if ((int)blockIdx.x < a.T) {
         if (wave == 0) route_token<LBF16, EC>(a, blockIdx.x, lane);
@@ -204,18 +206,22 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     const int groups = full + (tail > 0 ? 1 : 0);
     const int tile0 = run * a.tile_run, ntile = min(a.tile_run, a.tiles - tile0);
     struct Pair {
-        MxGroup g, u;
+        MxGroup t[2];  // a tile of gate rows and one of up rows
     };
-    // the wave's (tile, group) items, in order: group wave + kUpWaves j of tile 0, 1, ...
-    auto load_w = [&](int tile, int g) -> Pair {
+    // the wave's items: groups wave, wave + kUpWaves, ... of tile 0, 1, ...
+    const int gw = wave < groups ? (groups - wave + kUpWaves - 1) / kUpWaves : 0, items = ntile * gw;
+    auto load_w = [&](int it) -> Pair {
+        const int tile = XREG ? it : it / gw, g = XREG ? wave : wave + it % gw * kUpWaves;
         const int64_t row = (int64_t)e * 2 * a.I + (tile0 + tile) * 16 + r;
         const uint8_t *gc = a.gu_codes + row * (a.H / 2), *gs = a.gu_scales + row * kb;
         const uint8_t *uc = gc + (int64_t)a.I * (a.H / 2), *us = gs + (int64_t)a.I * kb;
-        if (g < full) return Pair{load_mx_group(gc, gs, g, lg), load_mx_group(uc, us, g, lg)};
-        return Pair{load_mx_tail(gc, gs, g, lg, tail), load_mx_tail(uc, us, g, lg, tail)};
+        if (g < full) return Pair{{load_mx_group(gc, gs, g, lg), load_mx_group(uc, us, g, lg)}};
+        return Pair{{load_mx_tail(gc, gs, g, lg, tail), load_mx_tail(uc, us, g, lg, tail)}};
     };
-    Pair w{};
-    if (wave < groups) w = load_w(0, wave);  // in flight while the tokens are looked up
+    // two items in flight while the tokens are looked up
+    Pair w{}, w1{};
+    if (items > 0) w = load_w(0);
+    if (items > 1) w1 = load_w(1);
 
     // the tokens that chose e
     for (int t = wave; t < a.T; t += kUpWaves) {
@@ -242,56 +248,64 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     if (in && wave == 0) sh_tok[at] = lane;
     __syncthreads();
 
-    const int nct = (n + 15) / 16;
-    const __bf16 *xr[NC];
-#pragma unroll
-    for (int c = 0; c < NC; c++)  // columns past the last token repeat the first; they are not stored
-        xr[c] = a.x + (int64_t)sh_tok[c * 16 + r < n ? c * 16 + r : 0] * a.ld_x;
-    for (int tile = 0; tile < ntile; tile++) {
-        f32x4 ag[NC] = {}, au[NC] = {};
-        for (int g = wave; g < groups; g += kUpWaves) {
-            const bool last = g + kUpWaves >= groups;
-            auto load_x = [&](int c) { return g < full ? load_bf16_group(xr[c], g, lg) : load_bf16_tail(xr[c], g, lg, tail); };
-            // loads return in order: the activations, which come from L2, go ahead of the next weights
-            Bf16Group x = load_x(0);
-            __builtin_amdgcn_sched_barrier(0);
-            const Pair next = load_w(last ? min(tile + 1, ntile - 1) : tile, last ? wave : g + kUpWaves);
-            __builtin_amdgcn_sched_barrier(0);
-            group_product(w.g, x, lg, ag[0]);
-            group_product(w.u, x, lg, au[0]);
-#pragma unroll
-            for (int c = 1; c < NC; c++)
-                if (c < nct) {
-                    x = load_x(c);
-                    group_product(w.g, x, lg, ag[c]);
-                    group_product(w.u, x, lg, au[c]);
-                }
-            w = next;
+    // Sixteen tokens at a time; more read the weights again, which are in the caches then.
+    for (int q = 0; q < n; q += 16) {
+        const int cols = min(16, n - q);
+        // columns past the last token repeat the first; their results are not stored
+        const __bf16 *xr = a.x + (int64_t)sh_tok[q + (r < cols ? r : 0)] * a.ld_x;
+        auto load_x = [&](int g) { return g < full ? load_bf16_group<false>(xr, g, lg) : load_bf16_group<true>(xr, g, lg, tail); };
+        Bf16Group x;
+        if (XREG && gw > 0) x = load_x(wave);
+        if (q > 0) {
+            if (items > 0) w = load_w(0);
+            if (items > 1) w1 = load_w(1);
         }
-        if (tile > 0) __syncthreads();  // the previous tile's sums have been read
+        int it = 0;
+        for (int c0 = 0; c0 < ntile; c0 += kUpTiles) {
+            f32x4 acc[kUpTiles][2] = {};
 #pragma unroll
-        for (int c = 0; c < NC; c++)
-            if (c < nct) {
-                *reinterpret_cast<f32x4 *>(&red[wave][0][c][lane * 4]) = ag[c];
-                *reinterpret_cast<f32x4 *>(&red[wave][1][c][lane * 4]) = au[c];
+            for (int t = 0; t < kUpTiles; t++) {
+                if (c0 + t >= ntile) break;
+                for (int j = 0; j < gw; j++, it++) {
+                    if constexpr (!XREG) x = load_x(wave + j * kUpWaves);
+                    if (it + 2 < items) {
+                        // loads return in order: the activations, which come from L2, go ahead
+                        __builtin_amdgcn_sched_barrier(0);
+                        const Pair w2 = load_w(it + 2);
+                        __builtin_amdgcn_sched_barrier(0);
+                        group_product<2>(w.t, x, lg, acc[t]);
+                        w = w1;
+                        w1 = w2;
+                    } else {
+                        group_product<2>(w.t, x, lg, acc[t]);
+                        w = w1;
+                    }
+                }
             }
-        __syncthreads();
-        // element (row il of the tile, column j) sits in lane j % 16 + 16 (il / 4), register il % 4
-        for (int o = tid; o < n * 16; o += 64 * kUpWaves) {
-            const int il = o % 16, j = o / 16;
-            const int src = (j % 16 + 16 * (il / 4)) * 4 + il % 4;
-            float gs = 0.0f, us = 0.0f;
+            if (c0 > 0 || q > 0) __syncthreads();  // the previous sums have been read
 #pragma unroll
-            for (int v = 0; v < kUpWaves; v++) {
-                gs += red[v][0][j / 16][src];
-                us += red[v][1][j / 16][src];
+            for (int t = 0; t < kUpTiles; t++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) *reinterpret_cast<f32x4 *>(&red[wave][t][i][lane * 4]) = acc[t][i];
+            __syncthreads();
+            // element (row il of a tile, column j) sits in lane j + 16 (il / 4), register il % 4
+            const int rows = min(kUpTiles, ntile - c0) * 16;
+            for (int o = tid; o < cols * rows; o += 64 * kUpWaves) {
+                const int ir = o % rows, j = o / rows, il = ir % 16;
+                const int src = (j + 16 * (il / 4)) * 4 + il % 4;
+                float gs = 0.0f, us = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kUpWaves; v++) {
+                    gs += red[v][ir / 16][0][src];
+                    us += red[v][ir / 16][1][src];
+                }
+                const int t = sh_tok[q + j];
+                const float h = silu(gs) * us * sh_p[t];
+                const __bf16 hi = (__bf16)h;
+                __bf16 *dst = a.h + (int64_t)(t * a.k + sh_rank[t]) * 2 * a.I + (tile0 + c0) * 16 + ir;
+                dst[0] = hi;
+                dst[a.I] = (__bf16)(h - (float)hi);
             }
-            const int t = sh_tok[j];
-            const float h = silu(gs) * us * sh_p[t];
-            const __bf16 hi = (__bf16)h;
-            __bf16 *dst = a.h + (int64_t)(t * a.k + sh_rank[t]) * 2 * a.I + (tile0 + tile) * 16 + il;
-            dst[0] = hi;
-            dst[a.I] = (__bf16)(h - (float)hi);
         }
     }
 }
@@ -331,43 +345,58 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
     const int kb = a.I / kMxBlock, full = a.I / kGroup, tail = kb - full * kGroupBlocks;
     const int groups = full + (tail > 0 ? 1 : 0), items = total * groups;
     const int n0 = blockIdx.x * 16;
-    auto load_w = [&](int it) -> MxGroup {
+    struct Tile {
+        MxGroup t[1];
+    };
+    auto load_w = [&](int it) -> Tile {
         const int g = it % groups;
         const int64_t row = (int64_t)(sh_info[it / groups] >> 16) * a.H + n0 + r;
         const uint8_t *c = a.dn_codes + row * (a.I / 2), *s = a.dn_scales + row * kb;
-        return g < full ? load_mx_group(c, s, g, lg) : load_mx_tail(c, s, g, lg, tail);
+        if (g < full) return Tile{{load_mx_group(c, s, g, lg)}};
+        return Tile{{load_mx_tail(c, s, g, lg, tail)}};
     };
     // the lane's token (and choice) in pass q of an item's tokens
     auto load_tok = [&](int it, int q) -> int {
         const int at = it / groups, n = sh_info[at] & 0xFFFF, j = q * kDownTokens + r % kDownTokens;
         return a.slot_tok[sh_list[at] * a.T + (j < n ? j : 0)];
     };
-    MxGroup w{};
+    // two items in flight ahead
+    Tile w{}, w1{};
     int tok = 0;
     if (wave < items) {
-        tok = load_tok(wave, 0);
         w = load_w(wave);
+        tok = load_tok(wave, 0);
     }
+    if (wave + kDownWaves < items) w1 = load_w(wave + kDownWaves);
     for (int it = wave; it < items; it += kDownWaves) {
         const int g = it % groups, n = __builtin_amdgcn_readfirstlane(sh_info[it / groups] & 0xFFFF);
-        const int passes = (n + kDownTokens - 1) / kDownTokens, nx = min(it + kDownWaves, items - 1);
-        MxGroup next;
-        int next_tok;
+        const int passes = (n + kDownTokens - 1) / kDownTokens;
         for (int q = 0; q < passes; q++) {
             const __bf16 *row = a.h + ((int64_t)((tok & 255) * a.k + (tok >> 8)) * 2 + plane) * a.I;
-            const Bf16Group h = g < full ? load_bf16_group(row, g, lg) : load_bf16_tail(row, g, lg, tail);
-            __builtin_amdgcn_sched_barrier(0);
-            // loads return in order: what the next pass or item needs goes behind
+            Bf16Group h;
+            if (g < full) h = load_bf16_group<false>(row, g, lg);
+            else h = load_bf16_group<true>(row, g, lg, tail);
             const int t = tok & 255;
+            f32x4 one[1] = {};
+            // loads return in order: what the next pass or item needs goes behind
+            __builtin_amdgcn_sched_barrier(0);
             if (q + 1 < passes) {
                 tok = load_tok(it, q + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                group_product<1>(w.t, h, lg, one);
+            } else if (it + 2 * kDownWaves < items) {
+                tok = load_tok(it + kDownWaves, 0);
+                const Tile w2 = load_w(it + 2 * kDownWaves);
+                __builtin_amdgcn_sched_barrier(0);
+                group_product<1>(w.t, h, lg, one);
+                w = w1;
+                w1 = w2;
             } else {
-                next_tok = load_tok(nx, 0);
-                next = load_w(nx);
+                if (it + kDownWaves < items) tok = load_tok(it + kDownWaves, 0);
+                group_product<1>(w.t, h, lg, one);
+                w = w1;
             }
-            __builtin_amdgcn_sched_barrier(0);
-            f32x4 acc = {};
-            group_product(w, h, lg, acc);
+            f32x4 acc = one[0];
             // columns c and c + 8 of a row of 16 lanes
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -381,8 +410,6 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
                 *dst = s;
             }
         }
-        w = next;
-        tok = next_tok;
     }
     __syncthreads();
     OT *y = reinterpret_cast<OT *>(a.y);
@@ -399,19 +426,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-template <bool LBF16, int NC>
-void launch_up_e(const MoeDev &a, hipStream_t stream) {
+template <bool LBF16, bool XREG>
+void launch_up_x(const MoeDev &a, hipStream_t stream) {
     const dim3 grid((unsigned)(a.T + a.slots * a.runs)), block(64 * kUpWaves);
-    if (a.E <= 64) hipLaunchKernelGGL((k_moe_up<LBF16, 1, NC>), grid, block, 0, stream, a);
-    else if (a.E <= 128) hipLaunchKernelGGL((k_moe_up<LBF16, 2, NC>), grid, block, 0, stream, a);
-    else if (a.E <= 256) hipLaunchKernelGGL((k_moe_up<LBF16, 4, NC>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((k_moe_up<LBF16, 8, NC>), grid, block, 0, stream, a);
+    if (a.E <= 64) hipLaunchKernelGGL((k_moe_up<LBF16, 1, XREG>), grid, block, 0, stream, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((k_moe_up<LBF16, 2, XREG>), grid, block, 0, stream, a);
+    else if (a.E <= 256) hipLaunchKernelGGL((k_moe_up<LBF16, 4, XREG>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((k_moe_up<LBF16, 8, XREG>), grid, block, 0, stream, a);
 }
 
 template <bool LBF16>
 void launch_up(const MoeDev &a, hipStream_t stream) {
-    if (a.T <= 16) launch_up_e<LBF16, 1>(a, stream);
-    else launch_up_e<LBF16, 4>(a, stream);
+    if (a.H <= kUpWaves * kGroup) launch_up_x<LBF16, true>(a, stream);
+    else launch_up_x<LBF16, false>(a, stream);
 }
 
 }  // namespace
@@ -453,8 +480,8 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     a.pair_slots = a.T * a.k < a.E ? 1 : 0;
     a.slots = a.pair_slots ? a.T * a.k : a.E;
     a.tiles = a.I / 16;
-    // tiles per workgroup: several where the slots give the device more than eight workgroups per CU
-    a.tile_run = std::min(8, std::max(1, (int)((int64_t)a.slots * a.tiles / (8 * num_cus))));
+    // tiles per workgroup: an even share of one round over the device, at most 8
+    a.tile_run = (int)std::min<int64_t>(8, std::max<int64_t>(1, ((int64_t)a.slots * a.tiles + num_cus - 1) / num_cus));
     a.runs = (a.tiles + a.tile_run - 1) / a.tile_run;
     if (p.logits_bf16) launch_up<true>(a, stream);
     else launch_up<false>(a, stream);

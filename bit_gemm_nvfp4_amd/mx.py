@@ -15,7 +15,7 @@ from . import (_DT, _I32, _I64, _P, _SIGNATURES, _RESTYPES, _SZ, _check, _rows, 
 
 MX_OP_GEMM_BF16, MX_OP_GEMM_MX, MX_OP_MOE = 0, 1, 2
 MX_BLOCK = 32
-SKINNY_MAX_M = 64  # products of up to this many rows take no workspace
+SKINNY_MAX_M = 16  # products of up to this many rows take no workspace
 MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 64, 512, 16
 MX_EXPORTED = ["mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_moe", "mxfp4_workspace_size"]
 
