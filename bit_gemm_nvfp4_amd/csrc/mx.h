@@ -140,7 +140,7 @@ hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M
                           void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,
                           int num_cus, hipStream_t stream);
 
-size_t mx_moe_ws_bytes(int64_t tokens, int64_t top_k, int64_t inter);
+size_t mx_moe_ws_bytes(int64_t pairs, int64_t hidden, int64_t inter);
 struct MoeArgs {
     const void *x;
     int64_t tokens, ld_x;

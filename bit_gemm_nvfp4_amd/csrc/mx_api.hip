@@ -58,7 +58,7 @@ size_t mxfp4_workspace_size(int op, int64_t m, int64_t n, int64_t k) {
     case MXFP4_OP_GEMM_BF16: return mx_gemm_ws_bytes(m, n, k, false, cus > 0 ? cus : 256);
     case MXFP4_OP_GEMM_MX: return mx_gemm_ws_bytes(m, n, k, true, cus > 0 ? cus : 256);
     case MXFP4_OP_MOE:
-        if (m > MXFP4_MOE_MAX_TOKENS || n > MXFP4_MOE_MAX_TOP_K) return 0;
+        if (m > MXFP4_MOE_MAX_TOKENS * MXFP4_MOE_MAX_TOP_K) return 0;
         return mx_moe_ws_bytes(m, n, k);
     default: return 0;
     }
@@ -109,7 +109,7 @@ nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
     } else {
         st = check_rows(a_bf16, M, K, lda, 2, 16);
         if (st != NVFP4_OK) return st;
-        if (M > 64 && lda > kMaxTileLd) return NVFP4_ERR_SHAPE;
+        if (M > 16 && lda > kMaxTileLd) return NVFP4_ERR_SHAPE;
     }
     const int eb = elem_bytes(c_dtype);
     st = check_rows(c, M, N, ldc, eb, eb);
@@ -147,7 +147,7 @@ nvfp4_status mxfp4_moe(const void *x, int64_t tokens, int64_t ld_x, const void *
     st = check_rows(y, tokens, H, ld_y, yeb, yeb);
     if (st != NVFP4_OK) return st;
     if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
-    if (tokens > 0 && (!workspace || workspace_bytes < mx_moe_ws_bytes(tokens, top_k, I))) return NVFP4_ERR_WORKSPACE;
+    if (tokens > 0 && (!workspace || workspace_bytes < mx_moe_ws_bytes(tokens * top_k, H, I))) return NVFP4_ERR_WORKSPACE;
     const int cus = current_device_cus();
     if (cus == 0) return NVFP4_ERR_DEVICE;
     if (tokens == 0) return NVFP4_OK;

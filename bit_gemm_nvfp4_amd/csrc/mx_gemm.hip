@@ -535,18 +535,29 @@ struct MxPlan {
 //   W4A4   512 x 12288 x 4096   256x256: 33.1   128x256: 23.8 *  128x128: 29.9   64x128: 34.6
 //   W4A4   512 x 4096 x 12288   256x256: 81.5   128x256: 52.2    128x128 in two slices: 31.1 * (one: 35.8)
 //   W4A4   4096 x 4096 x 4096   256x256: 40.1 * 128x256: 45.2    128x128: 54.1   64x128: 60.8
-//   W4A4   200 x 1000 x 2048    256x256: 19.4   128x256: 13.7    128x128: 9.2 *  64x128: 7.6
+//   W4A4   64 x 12288 x 4096    64x128: 15.6    64x64: 10.8 *  32x64: 11.8
+//   W4A4   128 x 4096 x 4096    128x128: 13.0   64x128: 12.5   64x64: 9.6 *
 //   W4A16  512 x 12288 x 4096   256x256: 81.4   128x256: 50.1 *  128x128: 55.5   64x128: 60.3
 //   W4A16  512 x 4096 x 12288   128x256: 128.4, in four slices 59.1 *  128x128 in two: 64.2
-//   W4A16  128 x 4096 x 4096    128x128: 35.6   64x128: 26.5, in four slices 17.9 *
+//   W4A16  128 x 4096 x 4096    128x128: 35.6   64x128: 24.6, in four slices 16.9 *  32x128 in two: 17.3
+//   W4A16  17 x 12288 x 4096    64x128: 24.7, in four slices 16.6   32x128: 21.0, in four slices 14.8 *
 //   W4A16  4096 x 12288 x 4096  256x256: 313 *  128x256: 359     128x128: 361
 struct TileCost {
     int bm, bn, per_cu;
     double start, window, window_full;
 };
-constexpr TileCost kTileCost[2][4] = {
-    {{256, 256, 1, 3.0, 12.6, 12.6}, {128, 256, 1, 5.0, 6.4, 6.4}, {128, 128, 2, 4.0, 4.0, 7.0}, {64, 128, 2, 3.0, 2.95, 4.5}},
-    {{256, 256, 1, 7.8, 3.84, 3.84}, {128, 256, 1, 5.0, 2.5, 2.5}, {128, 128, 1, 2.5, 1.45, 1.45}, {64, 128, 2, 2.5, 1.6, 1.8}},
+constexpr int kTileShapes = 5;
+constexpr TileCost kTileCost[2][kTileShapes] = {
+    {{256, 256, 1, 3.0, 12.6, 12.6},
+     {128, 256, 1, 5.0, 6.4, 6.4},
+     {128, 128, 2, 4.0, 4.0, 7.0},
+     {64, 128, 2, 3.0, 2.8, 4.5},
+     {32, 128, 2, 3.0, 2.1, 3.0}},
+    {{256, 256, 1, 7.8, 3.84, 3.84},
+     {128, 256, 1, 5.0, 2.5, 2.5},
+     {128, 128, 1, 2.5, 1.45, 1.45},
+     {64, 64, 2, 2.4, 0.95, 1.3},
+     {0, 0, 0, 0, 0, 0}},  // no fifth shape
 };
 constexpr int kMaxSplits = 8;
 constexpr double kReduceStart = 4.0, kReduceBytesPerUs = 3.0e6;  // the pass that adds the slices
@@ -555,8 +566,9 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
     const int64_t windows = (K + kGroup - 1) / kGroup;
     MxPlan best{0, 1, (int)windows};
     double cost = 1e30;
-    for (int cfg = 0; cfg < 4; cfg++) {
+    for (int cfg = 0; cfg < kTileShapes; cfg++) {
         const TileCost &t = kTileCost[a_mx ? 1 : 0][cfg];
+        if (t.bm == 0) continue;
         const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
         for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplits, windows); s++) {
             const int64_t per = (windows + s - 1) / s;
@@ -621,14 +633,15 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
         case 0: launch_tile_t<MxTile<256, 256, 2, 4, true, 2>, OT>(p, plan.splits, workspace, stream); break;
         case 1: launch_tile_t<MxTile<128, 256, 2, 4, true, 3>, OT>(p, plan.splits, workspace, stream); break;
         case 2: launch_tile_t<MxTile<128, 128, 4, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
-        default: launch_tile_t<MxTile<64, 128, 2, 2, true, 2>, OT>(p, plan.splits, workspace, stream); break;
+        default: launch_tile_t<MxTile<64, 64, 2, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
         }
     } else {
         switch (plan.cfg) {
         case 0: launch_tile_t<MxTile<256, 256, 2, 4, false, 3>, OT>(p, plan.splits, workspace, stream); break;
         case 1: launch_tile_t<MxTile<128, 256, 2, 4, false, 3>, OT>(p, plan.splits, workspace, stream); break;
         case 2: launch_tile_t<MxTile<128, 128, 2, 2, false, 3>, OT>(p, plan.splits, workspace, stream); break;
-        default: launch_tile_t<MxTile<64, 128, 1, 4, false, 4>, OT>(p, plan.splits, workspace, stream); break;
+        case 3: launch_tile_t<MxTile<64, 128, 1, 4, false, 4>, OT>(p, plan.splits, workspace, stream); break;
+        default: launch_tile_t<MxTile<32, 128, 1, 4, false, 4>, OT>(p, plan.splits, workspace, stream); break;
         }
     }
 }
@@ -642,14 +655,29 @@ void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int
                        A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, w->rows, (int)w->cols, c, ldc);
 }
 
+// W row tiles per wave and waves per workgroup.  bf16 activations cost L2 traffic in every workgroup (2 M K
+// bytes), so wide products share them between tiles once that leaves enough workgroups; MXFP4 ones are a
+// quarter of that.  Measured (us, K = 4096 unless said; best in each row is what the rule picks, or within 3 %):
+//   bf16  16 x 12288: 1 tile 17.1 (2 waves), 2 tiles 15.3, 4 tiles x 8 waves 12.2;  1 x 12288: 9.5, 10.0, 9.0
+//   bf16  16 x 6000:  1 tile 11.9, 2 tiles x 4 waves 8.8, 4 tiles 11.4;             8 x 8192: 9.2, 7.3, 9.7
+//   bf16  16 x 4096:  1 tile 7.3, 2 tiles 8.5;      13 x 4096, K = 12288: 1 tile 15.1 (4 waves), 2 tiles 18.4
+//   MXFP4 16 x 12288: 1 tile x 4 waves 9.6, 4 tiles x 8 waves 9.3;  1 x 12288: 7.3, 7.8;  16 x 4096: 4.8, 8.7
 template <bool A_MX, class OT>
 void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
                    int64_t ldc, int num_cus, hipStream_t stream) {
-    const int64_t groups = (w->cols + kGroup - 1) / kGroup;
-    // enough waves to keep about 12 per CU streaming, no more than there are groups to share out
-    int waves = 4;
-    if ((w->rows + 15) / 16 * waves < 12 * (int64_t)num_cus) waves = 8;
-    while (waves > 1 && waves / 2 >= groups) waves /= 2;
+    const int64_t N = w->rows, groups = (w->cols + kGroup - 1) / kGroup;
+    int waves = 4, tiles = 1;
+    if (!A_MX && N >= 48 * (int64_t)num_cus) {
+        tiles = 4;
+        waves = 8;
+    } else if (!A_MX && N > 16 * (int64_t)num_cus) {
+        tiles = 2;
+    }
+    while (waves > 1 && waves / 2 >= groups) waves /= 2;  // no more waves than groups to share out
+    if constexpr (!A_MX) {
+        if (tiles == 4) return launch_skinny_t<4, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
+        if (tiles == 2) return launch_skinny_t<2, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
+    }
     launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
 }
 

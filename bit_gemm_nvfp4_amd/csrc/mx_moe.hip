@@ -48,6 +48,9 @@ struct MoeDev {
     int32_t *slot_n;     // [slots] tokens of the slot | expert << 16
     uint16_t *slot_tok;  // [slots][T] token | choice << 8
     __bf16 *h;           // [T * k][2][I]: the two planes of a (token, choice)
+    float *parts;        // [workgroups of k_moe_down][T][64], with several tokens per expert
+    uint32_t *arrived;   // [64-row blocks of H], zeroed by k_moe_up
+    int row_blocks;
     int T, E, k, renorm, slots, pair_slots, tiles, tile_run, runs;
 };
 
@@ -179,6 +182,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if ((int)blockIdx.x < a.T) {
         if (wave == 0) route_token<LBF16, EC>(a, blockIdx.x, lane);
+        if (blockIdx.x == 0)
+            for (int j = tid; j < a.row_blocks; j += 64 * kUpWaves) a.arrived[j] = 0;
         return;
     }
     const int block = blockIdx.x - a.T;
@@ -311,116 +316,189 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
 }
 
 // Eight tokens at a time: columns 0-7 of the matrix instruction take the high planes of their h, columns 8-15
-// the low planes, and the two halves of the result are added.
+// the low planes, and the two halves of the result are added.  A unit of work is eight tokens of a slot and a
+// 512-column group; units are dealt to the waves in turn.
 constexpr int kDownTokens = 8;
+constexpr int kDownEntries = kMaxE + kMaxT * MXFP4_MOE_MAX_TOP_K / kDownTokens;
 
-template <class OT>
+// RT: tiles of 16 rows that share a unit's activations.  RT = 1: one workgroup has all the units of its rows.
+// RT = 4, for several tokens per expert: the h of all tokens passes through every workgroup, so fewer, taller
+// ones read less of it (64 tokens, 8 of 64 experts, 4096 x 1536: 131 us with RT = 1); RT workgroups then share
+// the units of 64 rows, each leaves its sums in the workspace, and the one that finishes last adds them in
+// order.
+template <class OT, int RT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
-    extern __shared__ __align__(16) float sums[];  // [waves][T][16]
-    __shared__ int sh_list[kMaxE], sh_info[kMaxE], sh_cnt[kDownWaves];
+    extern __shared__ __align__(16) float sums[];  // [waves][T][16 RT]
+    __shared__ uint32_t sh_entry[kDownEntries];    // slot | eight-token pass << 9 | tokens of the slot << 16
+    __shared__ int sh_expert[kMaxE], sh_cnt[kDownWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    static_assert(kMaxE <= 64 * kDownWaves, "one thread per slot");
-    // the slots with tokens, in order
+    static_assert(kMaxE <= 64 * kDownWaves && kMaxE <= 512, "one thread per slot, nine bits");
+    // entries in the order of the slots: the passes of the slots before give each its place
     const int info = tid < a.slots ? a.slot_n[tid] : 0;
-    const uint64_t m = __ballot(info != 0);
-    if (lane == 0) sh_cnt[wave] = __popcll(m);
-    float *mine = sums + wave * a.T * 16;
-    for (int j = lane; j < a.T * 16; j += 64) mine[j] = 0.0f;
+    const int n_slot = info & 0xFFFF, passes = (n_slot + kDownTokens - 1) / kDownTokens;
+    int upto = passes;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 63) sh_cnt[wave] = upto;
+    float *mine = sums + wave * a.T * 16 * RT;
+    for (int j = lane; j < a.T * 16 * RT; j += 64) mine[j] = 0.0f;
     __syncthreads();
-    int base = 0, total = 0;
+    int at = upto - passes, entries = 0;
 #pragma unroll
     for (int v = 0; v < kDownWaves; v++) {
-        if (v < wave) base += sh_cnt[v];
-        total += sh_cnt[v];
+        if (v < wave) at += sh_cnt[v];
+        entries += sh_cnt[v];
     }
-    if (info != 0) {
-        const int at = base + __popcll(m & ((1ull << lane) - 1));
-        sh_list[at] = tid;
-        sh_info[at] = info;
-    }
+    if (tid < a.slots) sh_expert[tid] = info >> 16;
+    for (int q = 0; q < passes; q++) sh_entry[at + q] = (uint32_t)(tid | q << 9 | n_slot << 16);
     __syncthreads();
-    total = __builtin_amdgcn_readfirstlane(total);
+    entries = __builtin_amdgcn_readfirstlane(entries);
 
     const int r = lane & 15, lg = lane >> 4, plane = r / kDownTokens;
     const int kb = a.I / kMxBlock, full = a.I / kGroup, tail = kb - full * kGroupBlocks;
-    const int groups = full + (tail > 0 ? 1 : 0), items = total * groups;
-    const int n0 = blockIdx.x * 16;
+    const int groups = full + (tail > 0 ? 1 : 0), units = entries * groups;
+    const int part = blockIdx.x % RT, n0 = blockIdx.x / RT * (16 * RT);
     struct Tile {
-        MxGroup t[1];
+        MxGroup t[RT];
     };
-    auto load_w = [&](int it) -> Tile {
-        const int g = it % groups;
-        const int64_t row = (int64_t)(sh_info[it / groups] >> 16) * a.H + n0 + r;
-        const uint8_t *c = a.dn_codes + row * (a.I / 2), *s = a.dn_scales + row * kb;
-        if (g < full) return Tile{{load_mx_group(c, s, g, lg)}};
-        return Tile{{load_mx_tail(c, s, g, lg, tail)}};
+    auto load_w = [&](int u) -> Tile {
+        const int g = u % groups;
+        const int64_t row0 = (int64_t)sh_expert[sh_entry[u / groups] & 511] * a.H;
+        Tile w;
+#pragma unroll
+        for (int t = 0; t < RT; t++) {
+            // H is a multiple of 32: rows past it repeat the last one, and are not stored
+            const int64_t row = row0 + (RT == 1 ? n0 + r : min(n0 + 16 * t + r, a.H - 1));
+            const uint8_t *c = a.dn_codes + row * (a.I / 2), *s = a.dn_scales + row * kb;
+            w.t[t] = g < full ? load_mx_group(c, s, g, lg) : load_mx_tail(c, s, g, lg, tail);
+        }
+        return w;
     };
-    // the lane's token (and choice) in pass q of an item's tokens
-    auto load_tok = [&](int it, int q) -> int {
-        const int at = it / groups, n = sh_info[at] & 0xFFFF, j = q * kDownTokens + r % kDownTokens;
-        return a.slot_tok[sh_list[at] * a.T + (j < n ? j : 0)];
+    // the lane's token | choice << 8; columns past the last token repeat the first (not used in the end)
+    auto load_tok = [&](int u) -> int {
+        const uint32_t en = sh_entry[u / groups];
+        const int j = (en >> 9 & 127) * kDownTokens + r % kDownTokens, n = en >> 16;
+        return a.slot_tok[(en & 511) * a.T + (j < n ? j : 0)] | (j < n ? 0 : 1 << 16);
     };
-    // two items in flight ahead
-    Tile w{}, w1{};
-    int tok = 0;
-    if (wave < items) {
-        w = load_w(wave);
-        tok = load_tok(wave, 0);
-    }
-    if (wave + kDownWaves < items) w1 = load_w(wave + kDownWaves);
-    for (int it = wave; it < items; it += kDownWaves) {
-        const int g = it % groups, n = __builtin_amdgcn_readfirstlane(sh_info[it / groups] & 0xFFFF);
-        const int passes = (n + kDownTokens - 1) / kDownTokens;
-        for (int q = 0; q < passes; q++) {
-            const __bf16 *row = a.h + ((int64_t)((tok & 255) * a.k + (tok >> 8)) * 2 + plane) * a.I;
-            Bf16Group h;
-            if (g < full) h = load_bf16_group<false>(row, g, lg);
-            else h = load_bf16_group<true>(row, g, lg, tail);
-            const int t = tok & 255;
-            f32x4 one[1] = {};
-            // loads return in order: what the next pass or item needs goes behind
-            __builtin_amdgcn_sched_barrier(0);
-            if (q + 1 < passes) {
-                tok = load_tok(it, q + 1);
-                __builtin_amdgcn_sched_barrier(0);
-                group_product<1>(w.t, h, lg, one);
-            } else if (it + 2 * kDownWaves < items) {
-                tok = load_tok(it + kDownWaves, 0);
-                const Tile w2 = load_w(it + 2 * kDownWaves);
-                __builtin_amdgcn_sched_barrier(0);
-                group_product<1>(w.t, h, lg, one);
-                w = w1;
-                w1 = w2;
-            } else {
-                if (it + kDownWaves < items) tok = load_tok(it + kDownWaves, 0);
-                group_product<1>(w.t, h, lg, one);
-                w = w1;
-            }
-            f32x4 acc = one[0];
+    auto load_h = [&](int u, int tok) -> Bf16Group {
+        const int g = u % groups;
+        const __bf16 *row = a.h + ((int64_t)((tok & 255) * a.k + (tok >> 8 & 255)) * 2 + plane) * a.I;
+        if (g < full) return load_bf16_group<false>(row, g, lg);
+        return load_bf16_group<true>(row, g, lg, tail);
+    };
+    auto product = [&](const Tile &w, const Bf16Group &h, int tok) {
+        f32x4 acc[RT] = {};
+        group_product<RT>(w.t, h, lg, acc);
+#pragma unroll
+        for (int t = 0; t < RT; t++) {
             // columns c and c + 8 of a row of 16 lanes
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const float v = acc[i];
-                acc[i] = v + u2f(dpp_u32<kDppRowRor8>(f2u(v)));
+                const float v = acc[t][i];
+                acc[t][i] = v + u2f(dpp_u32<kDppRowRor8>(f2u(v)));
             }
-            if (r < kDownTokens && q * kDownTokens + r < n) {
-                f32x4 *dst = reinterpret_cast<f32x4 *>(&mine[t * 16 + lg * 4]);
+            if (r < kDownTokens && tok >> 16 == 0) {
+                f32x4 *dst = reinterpret_cast<f32x4 *>(&mine[(tok & 255) * (16 * RT) + t * 16 + lg * 4]);
                 f32x4 s = *dst;
-                s += acc;
+                s += acc[t];
                 *dst = s;
             }
         }
+    };
+    constexpr int STEP = kDownWaves * RT;
+    const int u0 = part * kDownWaves + wave;
+    if constexpr (RT == 1) {
+        // Loads return in order, so they are issued in the order of use: behind a unit's product come the
+        // activations of the next unit, the token of the one after and its weights.
+        if (u0 < units) {
+            const int u1 = min(u0 + STEP, units - 1);
+            int tok = load_tok(u0), tok1 = load_tok(u1);
+            Tile w = load_w(u0), w1 = load_w(u1);
+            Bf16Group h = load_h(u0, tok);
+            int u = u0;
+            for (; u + 2 * STEP < units; u += STEP) {
+                const Bf16Group h1 = load_h(u + STEP, tok1);
+                const int tok2 = load_tok(u + 2 * STEP);
+                __builtin_amdgcn_sched_barrier(0);
+                const Tile w2 = load_w(u + 2 * STEP);
+                __builtin_amdgcn_sched_barrier(0);
+                product(w, h, tok);
+                tok = tok1;
+                tok1 = tok2;
+                w = w1;
+                w1 = w2;
+                h = h1;
+            }
+            if (u + STEP < units) {
+                const Bf16Group h1 = load_h(u + STEP, tok1);
+                __builtin_amdgcn_sched_barrier(0);
+                product(w, h, tok);
+                tok = tok1;
+                w = w1;
+                h = h1;
+            }
+            product(w, h, tok);
+        }
+    } else if (u0 < units) {  // a unit's four tiles are enough to have one unit in flight ahead
+        int tok = load_tok(u0);
+        Tile w = load_w(u0);
+        int u = u0;
+        for (; u + STEP < units; u += STEP) {
+            const Bf16Group h = load_h(u, tok);
+            const int tok1 = load_tok(u + STEP);
+            __builtin_amdgcn_sched_barrier(0);
+            const Tile w1 = load_w(u + STEP);
+            __builtin_amdgcn_sched_barrier(0);
+            product(w, h, tok);
+            tok = tok1;
+            w = w1;
+        }
+        product(w, load_h(u, tok), tok);
     }
     __syncthreads();
     OT *y = reinterpret_cast<OT *>(a.y);
-    for (int o = tid; o < a.T * 16; o += 64 * kDownWaves) {
+    const int cells = a.T * 16 * RT;
+    // no expert: 0; a row with NaN or +inf has den = NaN
+    auto store_y = [&](int t, int n, float s) {
+        const float den = a.den[t];
+        y[(int64_t)t * a.ld_y + n] = (OT)(den == 0.0f ? 0.0f : s / den);
+    };
+    auto joined = [&](int o) {
         float s = 0.0f;
 #pragma unroll
-        for (int v = 0; v < kDownWaves; v++) s += sums[v * a.T * 16 + o];
-        const int t = o / 16;
-        const float den = a.den[t];
-        // no expert: 0; a row with NaN or +inf has den = NaN
-        y[(int64_t)t * a.ld_y + n0 + o % 16] = (OT)(den == 0.0f ? 0.0f : s / den);
+        for (int v = 0; v < kDownWaves; v++) s += sums[v * cells + o];
+        return s;
+    };
+    if constexpr (RT == 1) {
+        for (int o = tid; o < cells; o += 64 * kDownWaves) store_y(o / 16, n0 + o % 16, joined(o));
+    } else {
+        // Sums of the parts: written and read past the caches that are not shared between XCDs (relaxed
+        // atomics of agent scope).  Every wave waits for its stores before the workgroup counts itself in, so
+        // whoever counts RT - 1 before it finds all of them.
+        float *mine_p = a.parts + (int64_t)blockIdx.x * cells;
+        for (int o = tid; o < cells; o += 64 * kDownWaves)
+            __hip_atomic_store(mine_p + o, joined(o), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+        __syncthreads();
+        if (tid == 0)
+            sh_cnt[0] = (int)__hip_atomic_fetch_add(a.arrived + blockIdx.x / RT, 1u, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (sh_cnt[0] != RT - 1) return;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        const float *p = a.parts + (int64_t)(blockIdx.x - part) * cells;
+        for (int o = tid; o < cells; o += 64 * kDownWaves) {
+            const int t = o / (16 * RT), n = n0 + o % (16 * RT);
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < RT; v++)
+                s += __hip_atomic_load(p + (int64_t)v * cells + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (n < a.H) store_y(t, n, s);
+        }
     }
 }
 
@@ -441,12 +519,23 @@ void launch_up(const MoeDev &a, hipStream_t stream) {
     else launch_up_x<LBF16, false>(a, stream);
 }
 
+template <class OT, int RT>
+void launch_down(const MoeDev &a, int grid, hipStream_t stream) {
+    const size_t lds = (size_t)kDownWaves * a.T * 16 * RT * 4;  // at most 128 KiB
+    hipLaunchKernelGGL((k_moe_down<OT, RT>), dim3((unsigned)grid), dim3(64 * kDownWaves), lds, stream, a);
+}
+
+// Tokens per expert, on average, from which k_moe_down takes its tall form.
+constexpr int kTallTokens = 2;
+
 }  // namespace
 
-size_t mx_moe_ws_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
-    if (tokens <= 0 || top_k <= 0 || inter < 0) return 0;
-    return align256(kMaxT * 4) + align256(kMaxE * 4) + align256((size_t)kMaxE * tokens * 2) +
-           align256((size_t)tokens * top_k * inter * 4);
+// Sized from the number of (token, choice) pairs, which bounds the tokens.
+size_t mx_moe_ws_bytes(int64_t pairs, int64_t hidden, int64_t inter) {
+    if (pairs <= 0 || hidden <= 0 || inter <= 0) return 0;
+    const size_t tokens = (size_t)std::min<int64_t>(pairs, kMaxT), blocks = (size_t)(hidden + 63) / 64;
+    return align256(kMaxT * 4) + align256(kMaxE * 4) + align256(kMaxE * tokens * 2) +
+           align256((size_t)pairs * inter * 4) + align256(blocks * 4) + blocks * 4 * tokens * 64 * 4;
 }
 
 hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStream_t stream) {
@@ -477,18 +566,27 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     a.slot_tok = reinterpret_cast<uint16_t *>(ws);
     ws += align256((size_t)kMaxE * a.T * 2);
     a.h = reinterpret_cast<__bf16 *>(ws);
+    ws += align256((size_t)a.T * a.k * a.I * 4);
+    const int blocks = (a.H + 63) / 64;
+    a.arrived = reinterpret_cast<uint32_t *>(ws);
+    a.parts = reinterpret_cast<float *>(ws + align256((size_t)blocks * 4));
     a.pair_slots = a.T * a.k < a.E ? 1 : 0;
     a.slots = a.pair_slots ? a.T * a.k : a.E;
     a.tiles = a.I / 16;
     // tiles per workgroup: an even share of one round over the device, at most 8
     a.tile_run = (int)std::min<int64_t>(8, std::max<int64_t>(1, ((int64_t)a.slots * a.tiles + num_cus - 1) / num_cus));
     a.runs = (a.tiles + a.tile_run - 1) / a.tile_run;
+    const bool tall = a.T * a.k >= kTallTokens * a.E;
+    a.row_blocks = tall ? blocks : 0;
     if (p.logits_bf16) launch_up<true>(a, stream);
     else launch_up<false>(a, stream);
-    const dim3 down((unsigned)(a.H / 16));
-    const size_t lds = (size_t)kDownWaves * a.T * 16 * 4;
-    if (p.y_bf16) hipLaunchKernelGGL(k_moe_down<__bf16>, down, dim3(64 * kDownWaves), lds, stream, a);
-    else hipLaunchKernelGGL(k_moe_down<float>, down, dim3(64 * kDownWaves), lds, stream, a);
+    if (tall) {
+        if (p.y_bf16) launch_down<__bf16, 4>(a, blocks * 4, stream);
+        else launch_down<float, 4>(a, blocks * 4, stream);
+    } else {
+        if (p.y_bf16) launch_down<__bf16, 1>(a, a.H / 16, stream);
+        else launch_down<float, 1>(a, a.H / 16, stream);
+    }
     return hipGetLastError();
 }
 

@@ -184,10 +184,11 @@ def mx_gemm(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor, dtype: torch.dtype = 
     return out
 
 
-def mx_moe_workspace(tokens: int, top_k: int, w_down: MXFP4Tensor) -> torch.Tensor | None:
+def mx_moe_workspace(tokens: int, top_k: int, w_gate_up: MXFP4Tensor, w_down: MXFP4Tensor) -> torch.Tensor | None:
     """A workspace for mx_moe (None without tokens).  Its contents do not matter; calls that share one
     must be ordered (same stream, or events)."""
-    return _workspace(mx_workspace_size(MX_OP_MOE, tokens, top_k, w_down.shape[1]), w_down.codes.device)
+    nbytes = mx_workspace_size(MX_OP_MOE, tokens * top_k, w_gate_up.shape[1], w_down.shape[1])
+    return _workspace(nbytes, w_down.codes.device)
 
 
 def mx_moe(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_down: MXFP4Tensor, top_k: int,
@@ -214,7 +215,7 @@ def mx_moe(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_down
         ids = torch.empty((t, top_k), dtype=torch.int32, device=dev)
         weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = mx_moe_workspace(t, top_k, w_down)
+        workspace = mx_moe_workspace(t, top_k, w_gate_up, w_down)
     _call("mxfp4_moe", dev, x.data_ptr(), t, ld_x, logits.data_ptr(), _DT[logits.dtype], ld_l, logits.shape[1], top_k,
           1 if renormalize else 0, ctypes.byref(w_gate_up.c()), ctypes.byref(w_down.c()), out.data_ptr(), dt, ld_y,
           _opt(ids, dev, "ids"), _opt(weights, dev, "weights"), _opt(workspace, dev, "workspace"), _nbytes(workspace))

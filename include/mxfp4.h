@@ -38,7 +38,7 @@ typedef struct {
 enum {
     MXFP4_OP_GEMM_BF16 = 0, /* mxfp4_gemm with bf16 activations: (M, N, K)                     */
     MXFP4_OP_GEMM_MX = 1,   /* mxfp4_gemm with MXFP4 activations: (M, N, K)                    */
-    MXFP4_OP_MOE = 2        /* mxfp4_moe: (tokens, top_k, intermediate size)                   */
+    MXFP4_OP_MOE = 2        /* mxfp4_moe: (tokens * top_k, H, I)                               */
 };
 
 /* Largest arguments of mxfp4_moe. */
@@ -78,7 +78,7 @@ nvfp4_status mxfp4_dequantize(const mxfp4_tensor *in, void *out, nvfp4_dtype out
  * nothing elsewhere; a NaN block of W gives NaN in its column of C.
  * workspace (16-byte aligned, or NULL): with mxfp4_workspace_size(MXFP4_OP_GEMM_BF16 or _MX, M, N, K) bytes a
  * long K is split over workgroups where there are few output tiles (fp32 partial sums, added in slice
- * order); with less, or NULL, the product runs unsplit.  K <= 2^22, and for M > 64 lda <= 2^22
+ * order); with less, or NULL, the product runs unsplit.  K <= 2^22, and for M > 16 lda <= 2^22
  * (NVFP4_ERR_SHAPE).  K == 0 gives C = 0.
  */
 nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
@@ -106,7 +106,7 @@ nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
  * two bf16 planes (their value to 2^-17).  The result does not depend on the order of execution.
  * Errors: NVFP4_ERR_SHAPE for tokens > 64, experts > 512, top_k > 16 or operands that disagree;
  * NVFP4_ERR_ARG for top_k < 1, top_k > experts or a bad renormalize; NVFP4_ERR_WORKSPACE for less than
- * mxfp4_workspace_size(MXFP4_OP_MOE, tokens, top_k, I) bytes (16-byte aligned).
+ * mxfp4_workspace_size(MXFP4_OP_MOE, tokens * top_k, H, I) bytes (16-byte aligned).
  */
 nvfp4_status mxfp4_moe(const void *x, int64_t tokens, int64_t ld_x, const void *logits, nvfp4_dtype logits_dtype,
                        int64_t ld_logits, int64_t experts, int top_k, int renormalize, const mxfp4_tensor *w_gate_up,

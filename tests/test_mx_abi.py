@@ -36,13 +36,13 @@ def test_header_exports_and_binding_agree(nv):
 
 def test_workspace_sizes(nv):
     from bit_gemm_nvfp4_amd import mx
-    assert nv.mx_workspace_size(mx.MX_OP_GEMM_MX, 64, 4096, 4096) == 0
+    assert nv.mx_workspace_size(mx.MX_OP_GEMM_MX, 16, 4096, 12288) == 0
     assert nv.mx_workspace_size(mx.MX_OP_GEMM_BF16, 16, 4096, 4096) == 0
     # few output tiles and a long K: fp32 partial sums of at least two slices
     for op in (mx.MX_OP_GEMM_BF16, mx.MX_OP_GEMM_MX):
         assert nv.mx_workspace_size(op, 128, 256, 12288) >= 2 * 128 * 256 * 4
-    assert nv.mx_workspace_size(mx.MX_OP_MOE, 3, 2, 64) >= 3 * 2 * 64 * 4 + 3 * 2 * 4 + 3 * 4
-    for bad in ((0, -1, 1, 1), (0, 1 << 40, 1, 1), (99, 1, 1, 1), (mx.MX_OP_MOE, 65, 2, 64), (mx.MX_OP_MOE, 1, 17, 64)):
+    assert nv.mx_workspace_size(mx.MX_OP_MOE, 3 * 2, 96, 64) >= 3 * 2 * 64 * 4 + 3 * 2 * 4 + 3 * 4
+    for bad in ((0, -1, 1, 1), (0, 1 << 40, 1, 1), (99, 1, 1, 1), (mx.MX_OP_MOE, 64 * 16 + 1, 64, 64)):
         assert nv.mx_workspace_size(*bad) == 0
 
 
@@ -92,7 +92,7 @@ def test_gemm_refusals(nv):
 def test_moe_refusals(nv):
     f = nv.lib.mxfp4_moe
     E, H, I = 4, 64, 32
-    ws = nv.mx_workspace_size(2, 3, 2, I)
+    ws = nv.mx_workspace_size(2, 3 * 2, H, I)
 
     def call(x=P(FAKE), t=3, ldx=H, lg=P(FAKE), ldt=0, ldl=E, e=E, k=2, rn=1, gu=_mx(nv, E * 2 * I, H),
              dn=_mx(nv, E * H, I), y=P(FAKE), yd=1, ldy=H, ids=None, wt=None, w=P(FAKE), wsb=ws):

@@ -290,7 +290,8 @@ def _check_moe(nv, case, e, k, renorm, out="bf16"):
 
 MOE_CASES = [(1, 8, 2, 64, 32), (1, 1, 1, 32, 32), (1, 64, 8, 512, 96), (2, 5, 5, 96, 160), (3, 16, 3, 544, 64),
              (7, 4, 2, 128, 544), (16, 8, 2, 256, 64), (17, 130, 4, 64, 32), (33, 12, 3, 160, 96), (64, 8, 4, 96, 64),
-             (64, 512, 16, 32, 32), (50, 3, 1, 1056, 32)]
+             (64, 512, 16, 32, 32), (50, 3, 1, 1056, 32),
+             (64, 2, 2, 160, 1056), (12, 3, 2, 96, 544), (40, 8, 4, 4128, 96), (2, 1, 1, 32, 512)]
 
 
 @pytest.mark.parametrize("renorm", [True, False])
@@ -397,7 +398,7 @@ def test_graph_replays_with_kept_workspaces(nv):
     x, _, lt, _, gu, _, dn, _ = _moe_case(nv, 4, t, e, h, i)
     wl, _ = _weight(nv, np.random.default_rng(9), 200, 12288, 0.1)
     big, _ = _bf16(np.random.default_rng(2).standard_normal((130, 12288)))
-    ws_moe = nv.mx_moe_workspace(t, 2, dn)
+    ws_moe = nv.mx_moe_workspace(t, 2, gu, dn)
     ws_g = nv.mx_gemm_workspace(big, wl)
     qb = nv.mx_quantize(big)
     ws_q = nv.mx_gemm_workspace(qb, wl)
@@ -444,7 +445,7 @@ def test_int64_offsets(nv):
     codes[rows - 1] = 0x22
     codes[7] = 0x44
     w = nv.MXFP4Tensor(codes, scales)
-    for m in (1, 66):
+    for m in (1, 16, 17, 66):
         a = torch.ones((m, k), dtype=torch.bfloat16, device=DEV)
         c = nv.mx_gemm(a, w, dtype=torch.bfloat16)
         assert bool((c[:, rows - 1] == k).all()) and bool((c[:, 7] == 2 * k).all())
