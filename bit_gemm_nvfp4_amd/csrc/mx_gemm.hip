@@ -151,6 +151,7 @@ struct MxTile {
     static constexpr int LDS_BYTES = SC_OFF + 2 * SC_ROWS * 16;
     static constexpr int UNITS = STAGE / 1024, A_UNITS = W_OFF / 1024, UPW = UNITS / NW;
     static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    static constexpr bool WHOLE = TM <= 2;
     static constexpr int READS = TM + (A_MX ? TN : 0);  // LDS reads of a quarter's operands
     // epilogue: 32 rows of a wave's columns; rows 4 apart start 32 banks apart, so that the two halves of a
     // wave write different banks
@@ -238,7 +239,7 @@ __device__ __forceinline__ void mx_quarter(const MxFrags<T> &f, const int (&sa)[
 
 // Quarter q: elements 8 q .. 8 q + 7 of the two blocks of a step, W expanded to bf16 (bf16 A).
 template <class T>
-__device__ __forceinline__ void bf16_quarter(const MxFrags<T> &f, int q, const u32x4 (&w)[T::TN],
+__device__ __forceinline__ void bf16_quarter(const MxFrags<T> &f, int q, const u32x4 (&w)[T::A_MX ? 1 : T::TN],
                                              const float (&sb)[T::TN], f32x16 (&acc)[T::TM][T::TN]) {
     bf16x8 wf[T::TN];
 #pragma unroll
@@ -273,11 +274,37 @@ __device__ __forceinline__ void order_quarter() {
     __builtin_amdgcn_sched_group_barrier(0x008, T::TM * T::TN, 0);
 }
 
-// The main loop runs in quarters of a step with the operands of the next quarter read from LDS while the
-// matrix instructions of this one issue.  The step's one barrier stands before its last quarter, whose
-// operands are then in registers: behind it stage s + 1 is complete in LDS, so the first operands of
-// step s + 1 are read under the last quarter's instructions, and stage s may be overwritten, so the
-// loads of step s + NST are issued.
+// Everything a wave takes from LDS for one step.
+template <class T>
+struct MxStep {
+    MxFrags<T> q[4];
+    u32x4 w[T::A_MX ? 1 : T::TN];  // the W blocks (bf16 A)
+    int sa[T::TM], sb[T::TN];
+};
+
+// Instruction order of a whole step: the LDS reads spread evenly behind its matrix instructions.
+template <class T>
+__device__ __forceinline__ void order_step() {
+    constexpr int M = 4 * T::TM * T::TN;
+    constexpr int R = 4 * T::READS + (T::A_MX ? (T::TM + T::TN + 1) / 2 : 2 * T::TN);
+    constexpr int PER = (R + M - 1) / M;
+#pragma unroll
+    for (int i = 0; i < M; i++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+    }
+}
+
+// Main loop, two forms.
+// Wave tiles of two 32-row tiles or fewer (T::WHOLE) hold the operands of two whole steps: those of step s + 1
+// are read from LDS while the matrix instructions of step s issue, so a read has a whole step to arrive in.
+// The step's one barrier stands at its start: stage s + 1 is complete behind it, and stage s, all in
+// registers, may be overwritten.
+// Taller wave tiles have no registers for that and run in quarters of a step, with the operands of the next
+// quarter read while the matrix instructions of this one issue.  The barrier stands before the last quarter,
+// whose operands are then in registers: behind it stage s + 1 is complete, so the first operands of step s + 1
+// are read under the last quarter's instructions, and stage s may be overwritten.
+// W4A16 512 x 4096 x 12288 in quarters: 60.7 us; W4A4 512 x 12288 x 4096: 25.0 us.
 template <class T, class OT, bool SPLIT>
 __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(MxTileArgs p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
@@ -357,10 +384,7 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         for (int i = 0; i < T::TM; i++) f.a[i] = *reinterpret_cast<const u32x4 *>(pa + i * 32 * T::A_ROWB);
     };
     // what a whole step needs: scales, and with bf16 A the W blocks
-    int sa[T::TM], sb[T::TN];
-    float sf[T::TN];
-    u32x4 wblk[T::TN];
-    auto read_step = [&](int s) {
+    auto read_step = [&](int s, int (&sa)[T::TM], int (&sb)[T::TN], u32x4 (&wblk)[T::A_MX ? 1 : T::TN]) {
         const uint8_t *sc = lds + T::SC_OFF + ((w0 + s / T::WINDOW_STEPS) & 1) * (T::SC_ROWS * 16);
         const int in = s % T::WINDOW_STEPS;
         if constexpr (T::A_MX) {
@@ -381,7 +405,6 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     };
 
     f32x16 acc[T::TM][T::TN] = {};
-    MxFrags<T> f[2];
     load_scales(w0);
     put_scales(w0);
     load_scales(min(w0 + 1, windows - 1));
@@ -390,17 +413,65 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 1) * T::UPW, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_step(0);
-    read_frags(f[0], 0, 0);
-    for (int s = 0; s < nsteps; s++) {
-        // The loop's only branch stands before its first matrix instruction: with one between them the
-        // compiler moves them all behind it, and the operands of all four quarters stay live.
+    // The loops' only branches stand before a step's first matrix instruction: with one between them the
+    // compiler moves them all behind it, and the operands of the whole step stay live.
+    auto next_scales = [&](int s) {
         if (s % T::WINDOW_STEPS == T::WINDOW_STEPS - 1) {
             // the next window's scales, loaded a window ago; their buffer was last read two barriers ago
             const int win = w0 + s / T::WINDOW_STEPS;
             put_scales(win + 1);
             load_scales(min(win + 2, windows - 1));
         }
+    };
+    auto wait_stage = [&] {
+        // the next stage has landed when at most the loads of the NST - 2 later ones are outstanding
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 2) * T::UPW, 0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (T::WHOLE) {
+        auto read_all = [&](MxStep<T> &f, int s) {
+            read_step(s, f.sa, f.sb, f.w);
+#pragma unroll
+            for (int t = 0; t < 4; t++) read_frags(f.q[t], s, t);
+        };
+        auto step = [&](int s, const MxStep<T> &cur, MxStep<T> &next) {
+            next_scales(s);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_stage();
+            load_stage(s + T::NST);  // past the last step these load zeros or a part that is not read
+            read_all(next, s + 1);
+            if constexpr (T::A_MX) {
+                mx_quarter<T, 0>(cur.q[0], cur.sa, cur.sb, acc);
+                mx_quarter<T, 1>(cur.q[1], cur.sa, cur.sb, acc);
+                mx_quarter<T, 2>(cur.q[2], cur.sa, cur.sb, acc);
+                mx_quarter<T, 3>(cur.q[3], cur.sa, cur.sb, acc);
+            } else {
+                float sf[T::TN];
+#pragma unroll
+                for (int j = 0; j < T::TN; j++) sf[j] = scale_operand((uint32_t)cur.sb[j], 0);
+#pragma unroll
+                for (int t = 0; t < 4; t++) bf16_quarter<T>(cur.q[t], t, cur.w, sf, acc);
+            }
+            pin<T>(acc);
+            order_step<T>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        MxStep<T> f0, f1;
+        read_all(f0, 0);
+        for (int s = 0; s < nsteps; s += 2) {
+            step(s, f0, f1);
+            if (s + 1 < nsteps) step(s + 1, f1, f0);
+        }
+    } else {
+    int sa[T::TM], sb[T::TN];
+    float sf[T::TN];
+    u32x4 wblk[T::A_MX ? 1 : T::TN];
+    MxFrags<T> f[2];
+    read_step(0, sa, sb, wblk);
+    read_frags(f[0], 0, 0);
+    for (int s = 0; s < nsteps; s++) {
+        next_scales(s);
         if constexpr (!T::A_MX) {
 #pragma unroll
             for (int j = 0; j < T::TN; j++) sf[j] = scale_operand((uint32_t)sb[j], 0);
@@ -424,27 +495,24 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         pin<T>(acc);
         order_quarter<T, T::READS>();
         __builtin_amdgcn_sched_barrier(0);
-        // stage s + 1 has landed when at most the loads of the NST - 2 later stages are outstanding
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm((T::NST - 2) * T::UPW, 0));
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+        wait_stage();
         load_stage(s + T::NST);  // past the last step these load zeros or a part that is not read
         int pa[T::TM], pb[T::TN];
-        u32x4 pw[T::TN];
+        u32x4 pw[T::A_MX ? 1 : T::TN];
 #pragma unroll
         for (int i = 0; i < T::TM; i++) pa[i] = sa[i];
 #pragma unroll
-        for (int j = 0; j < T::TN; j++) {
-            pb[j] = sb[j];
-            pw[j] = wblk[j];
-        }
-        read_step(s + 1);
+        for (int j = 0; j < T::TN; j++) pb[j] = sb[j];
+#pragma unroll
+        for (int j = 0; j < (T::A_MX ? 1 : T::TN); j++) pw[j] = wblk[j];
+        read_step(s + 1, sa, sb, wblk);
         read_frags(f[0], s + 1, 0);
         if constexpr (T::A_MX) mx_quarter<T, 3>(f[1], pa, pb, acc);
         else bf16_quarter<T>(f[1], 3, pw, sf, acc);
         pin<T>(acc);
         order_quarter<T, T::READS + (T::A_MX ? (T::TM + T::TN + 1) / 2 : 2 * T::TN)>();
         __builtin_amdgcn_sched_barrier(0);
+    }
     }
     // no load may be in flight into the LDS of a workgroup that has ended
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
