@@ -23,6 +23,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kSkinnyMaxM = 16;
+constexpr int kMaxSplits = 8;  // K slices of a tiled product
 
 template <class OT>
 __device__ __forceinline__ void store_out(OT *p, float v) {
@@ -569,17 +570,30 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         }
 }
 
-// C = the sum of the K slices' partial planes, in slice order.
-template <class OT>
-__global__ __launch_bounds__(256) void k_mx_reduce(const float *__restrict__ P, int splits, int64_t M, int64_t N,
+// C = the sum of the K slices' partial planes, in slice order.  VEC columns per thread (4 where rows of the
+// planes and of C allow); the slices' loads are issued together.  Bound by reading the planes.
+template <class OT, int VEC>
+__global__ __launch_bounds__(256) void k_mx_reduce(const float *__restrict__ P, int splits, int64_t n, uint32_t cols,
                                                    OT *__restrict__ C, int64_t ldc) {
-    const int64_t n = M * N;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        float s = P[i];
-        for (int k = 1; k < splits; k++) s += P[k * n + i];
-        const int64_t m = i / N;
-        store_out(C + m * ldc + (i - m * N), s);
+    typedef float vec __attribute__((ext_vector_type(VEC)));
+    typedef OT out __attribute__((ext_vector_type(VEC)));
+    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    if (i >= n) return;
+    const float *p = P + i;
+    vec s = {};
+    for (int k = 0; k < splits; k += 4) {
+        vec v[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; j++, p += n)
+            if (k + j < splits) v[j] = *reinterpret_cast<const vec *>(p);
+#pragma unroll
+        for (int j = 0; j < 4; j++) s += v[j];
     }
+    out o;
+#pragma unroll
+    for (int q = 0; q < VEC; q++) o[q] = (OT)s[q];
+    const int64_t m = n <= 0xFFFFFFFFll ? (uint32_t)i / cols : i / cols;
+    *reinterpret_cast<out *>(C + m * ldc + (i - m * cols)) = o;
 }
 
 template <class OT>
@@ -600,11 +614,11 @@ struct MxPlan {
 // Tile shapes and what they cost: microseconds per tile (start, first loads, stores) and per window of 512
 // columns, with one workgroup per CU and with `per_cu` of them.  Fitted to timings of every shape with 1, 2
 // and 4 K slices on an MI355X; of those, in microseconds (tile: time; the shape picked is marked):
-//   W4A4   512 x 12288 x 4096   256x256: 33.1   128x256: 23.8 *  128x128: 29.9   64x128: 34.6
-//   W4A4   512 x 4096 x 12288   256x256: 81.5   128x256: 52.2    128x128 in two slices: 31.1 * (one: 35.8)
-//   W4A4   4096 x 4096 x 4096   256x256: 40.1 * 128x256: 45.2    128x128: 54.1   64x128: 60.8
-//   W4A4   64 x 12288 x 4096    64x128: 15.6    64x64: 10.8 *  32x64: 11.8
-//   W4A4   128 x 4096 x 4096    128x128: 13.0   64x128: 12.5   64x64: 9.6 *
+//   W4A4   512 x 12288 x 4096   256x256: 33.1   128x256: 23.9 *  128x128: 30.3   64x128: 29.8   64x64: 36.6
+//   W4A4   512 x 4096 x 12288   128x256: 53.4   128x128: 34.7 (two slices: 31.4)   64x128: 27.7 *  64x64: 32.4
+//   W4A4   4096 x 4096 x 4096   256x256: 40.1 * 128x256: 45.2    128x128: 54.1
+//   W4A4   1024 x 4096 x 4096   128x256: 20.2   128x128: 15.6 *  64x128: 18.6   64x64: 22.9
+//   W4A4   256 x 4096 x 4096    128x256: 18.7   128x128: 12.8    64x128: 10.0   64x64: 8.7 *
 //   W4A16  512 x 12288 x 4096   256x256: 81.4   128x256: 50.1 *  128x128: 55.5   64x128: 60.3
 //   W4A16  512 x 4096 x 12288   128x256: 128.4, in four slices 59.1 *  128x128 in two: 64.2
 //   W4A16  128 x 4096 x 4096    128x128: 35.6   64x128: 24.6, in four slices 16.9 *  32x128 in two: 17.3
@@ -622,12 +636,11 @@ constexpr TileCost kTileCost[2][kTileShapes] = {
      {64, 128, 2, 3.0, 2.8, 4.5},
      {32, 128, 2, 3.0, 2.1, 3.0}},
     {{256, 256, 1, 7.8, 3.84, 3.84},
-     {128, 256, 1, 5.0, 2.5, 2.5},
-     {128, 128, 1, 2.5, 1.45, 1.45},
-     {64, 64, 2, 2.4, 0.95, 1.3},
-     {0, 0, 0, 0, 0, 0}},  // no fifth shape
+     {128, 256, 1, 5.0, 2.4, 2.4},
+     {128, 128, 1, 2.5, 1.5, 1.5},
+     {64, 64, 2, 2.4, 0.82, 1.2},
+     {64, 128, 2, 2.5, 1.05, 1.8}},
 };
-constexpr int kMaxSplits = 8;
 constexpr double kReduceStart = 4.0, kReduceBytesPerUs = 3.0e6;  // the pass that adds the slices
 
 MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
@@ -636,7 +649,6 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
     double cost = 1e30;
     for (int cfg = 0; cfg < kTileShapes; cfg++) {
         const TileCost &t = kTileCost[a_mx ? 1 : 0][cfg];
-        if (t.bm == 0) continue;
         const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
         for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplits, windows); s++) {
             const int64_t per = (windows + s - 1) / s;
@@ -669,9 +681,14 @@ void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) 
     p.c = partial;
     p.vec_c = p.N % 4 == 0;
     hipLaunchKernelGGL((k_mx_tile<T, float, true>), grid, dim3(T::NT), 0, stream, p);
-    const int64_t blocks = std::min<int64_t>((p.M * p.N + 255) / 256, 8192);
-    hipLaunchKernelGGL(k_mx_reduce<OT>, dim3((unsigned)blocks), dim3(256), 0, stream,
-                       reinterpret_cast<const float *>(partial), splits, p.M, p.N, c, p.ldc);
+    const int64_t n = p.M * p.N;
+    const float *planes = reinterpret_cast<const float *>(partial);
+    if (p.vec_c && reinterpret_cast<uintptr_t>(c) % (4 * sizeof(OT)) == 0 && p.ldc % 4 == 0)
+        hipLaunchKernelGGL((k_mx_reduce<OT, 4>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream, planes,
+                           splits, n, (uint32_t)p.N, c, p.ldc);
+    else
+        hipLaunchKernelGGL((k_mx_reduce<OT, 1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, planes, splits,
+                           n, (uint32_t)p.N, c, p.ldc);
 }
 
 template <class OT>
@@ -701,7 +718,8 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
         case 0: launch_tile_t<MxTile<256, 256, 2, 4, true, 2>, OT>(p, plan.splits, workspace, stream); break;
         case 1: launch_tile_t<MxTile<128, 256, 2, 4, true, 3>, OT>(p, plan.splits, workspace, stream); break;
         case 2: launch_tile_t<MxTile<128, 128, 4, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
-        default: launch_tile_t<MxTile<64, 64, 2, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
+        case 3: launch_tile_t<MxTile<64, 64, 2, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
+        default: launch_tile_t<MxTile<64, 128, 2, 2, true, 3>, OT>(p, plan.splits, workspace, stream); break;
         }
     } else {
         switch (plan.cfg) {

@@ -71,14 +71,25 @@ class MXFP4Tensor:
 # The binding's own time is most of a small call's, so it takes the raw current stream of the device and
 # switches devices only when the tensors are not on the current one.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+_functions: dict = {}
+
+
+def _function(name: str):
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load_library(), name)
+    return fn
 
 
 def _call(name: str, device: torch.device, *args) -> None:
     """Call entry point `name` with `args` and the current stream of `device`.  The library launches on
     the current device, so `device` is made current for the call if it is not."""
-    fn = getattr(load_library(), name)
+    fn = _functions.get(name) or _function(name)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -125,12 +136,15 @@ def mx_quantize(x: torch.Tensor, src_scale: torch.Tensor | None = None, flags: t
     dev = x.device
     if out is None:
         out = MXFP4Tensor.empty(rows, cols, dev)
+        ct = CMXTensor(out.codes.data_ptr(), out.scales.data_ptr(), rows, cols)
     elif out.shape != (rows, cols) or out.codes.device != dev:
         raise AssertionError(f"out: shape {out.shape} on {out.codes.device}, expected {(rows, cols)} on {dev}")
+    else:
+        ct = out.c()
     if flags is None and check:
         flags = torch.zeros(1, dtype=torch.int32, device=dev)
     _call("mxfp4_quantize", dev, x.data_ptr(), _DT[x.dtype], ld, _opt(src_scale, dev, "src_scale", torch.float32),
-          ctypes.byref(out.c()), _opt(flags, dev, "flags", torch.int32))
+          ctypes.byref(ct), _opt(flags, dev, "flags", torch.int32))
     out.flags = flags
     if check:
         check_flags(flags, "mxfp4_quantize")
