@@ -741,30 +741,26 @@ void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int
                        A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, w->rows, (int)w->cols, c, ldc);
 }
 
-// W row tiles per wave and waves per workgroup.  bf16 activations cost L2 traffic in every workgroup (2 M K
-// bytes), so wide products share them between tiles once that leaves enough workgroups; MXFP4 ones are a
-// quarter of that.  Measured (us, K = 4096 unless said; best in each row is what the rule picks, or within 3 %):
-//   bf16  16 x 12288: 1 tile 17.1 (2 waves), 2 tiles 15.3, 4 tiles x 8 waves 12.2;  1 x 12288: 9.5, 10.0, 9.0
-//   bf16  16 x 6000:  1 tile 11.9, 2 tiles x 4 waves 8.8, 4 tiles 11.4;             8 x 8192: 9.2, 7.3, 9.7
-//   bf16  16 x 4096:  1 tile 7.3, 2 tiles 8.5;      13 x 4096, K = 12288: 1 tile 15.1 (4 waves), 2 tiles 18.4
-//   MXFP4 16 x 12288: 1 tile x 4 waves 9.6, 4 tiles x 8 waves 9.3;  1 x 12288: 7.3, 7.8;  16 x 4096: 4.8, 8.7
+// W row tiles per workgroup and its waves.  Every workgroup reads all of A through L2 (16 rows of bf16 are 3.8
+// times a tile of W), so tiles share it, as many as spread over the CUs in one round, up to three (four
+// spill).  Measured, us (K = 4096 unless said), the pick marked:
+//   bf16  16 x 12288: 1 tile 17.0, 2 tiles 15.2, 3 tiles 11.1 *, 4 tiles 12.0;  1 x 12288: 9.7, 10.0, 8.1 *, 9.0
+//   bf16  16 x 6000:  1 tile 11.9, 2 tiles 8.7 *, 3 tiles 10.0;   8 x 8192: 9.1, 7.4 *, 8.5
+//   bf16  16 x 4096:  1 tile 7.3 *, 2 tiles 8.5;   13 x 4096, K = 12288: 15.1 *, 18.3
+//   bf16  16 x 12288, K = 12288: 1 tile 45.4, 2 tiles 39.7, 3 tiles 27.5 *, 4 tiles 37.0
+//   MXFP4 16 x 12288: 9.6, 10.0, 8.2 *, 9.2;  1 x 12288: 7.2, 8.0, 7.1 *, 7.8;  16 x 6000: 7.0, 6.2 *, 7.3
+// Waves split K: 8 with three tiles (2 and 4 waves 11.3, 11.4 against 11.1), else 4 (8 x 8192: 2, 4, 8 waves 7.3,
+// 7.4, 7.6).
 template <bool A_MX, class OT>
 void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
                    int64_t ldc, int num_cus, hipStream_t stream) {
-    const int64_t N = w->rows, groups = (w->cols + kGroup - 1) / kGroup;
-    int waves = 4, tiles = 1;
-    if (!A_MX && N >= 48 * (int64_t)num_cus) {
-        tiles = 4;
-        waves = 8;
-    } else if (!A_MX && N > 16 * (int64_t)num_cus) {
-        tiles = 2;
-    }
+    const int64_t tiles = (w->rows + 15) / 16, groups = (w->cols + kGroup - 1) / kGroup;
+    const int64_t share = (tiles + num_cus - 1) / num_cus;
+    int waves = share >= 3 ? 8 : 4;
     while (waves > 1 && waves / 2 >= groups) waves /= 2;  // no more waves than groups to share out
-    if constexpr (!A_MX) {
-        if (tiles == 4) return launch_skinny_t<4, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
-        if (tiles == 2) return launch_skinny_t<2, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
-    }
-    launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
+    if (share >= 3) launch_skinny_t<3, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
+    else if (share == 2) launch_skinny_t<2, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
+    else launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
 }
 
 template <class OT>
