@@ -31,6 +31,8 @@ namespace {
 
 constexpr int kMaxT = MXFP4_MOE_MAX_TOKENS, kMaxE = MXFP4_MOE_MAX_EXPERTS;
 constexpr int kUpWaves = 8, kDownWaves = 8;
+// k_moe_down's tall form: row tiles per workgroup, and the average tokens per expert from which it is taken.
+constexpr int kTallTiles = 4, kTallTokens = 2, kTallRows = 16 * kTallTiles;
 constexpr int kUpTiles = 4;  // tiles whose sums a wave keeps before the waves join them
 
 struct MoeDev {
@@ -525,17 +527,14 @@ void launch_down(const MoeDev &a, int grid, hipStream_t stream) {
     hipLaunchKernelGGL((k_moe_down<OT, RT>), dim3((unsigned)grid), dim3(64 * kDownWaves), lds, stream, a);
 }
 
-// Tokens per expert, on average, from which k_moe_down takes its tall form.
-constexpr int kTallTokens = 2;
-
 }  // namespace
 
 // Sized from the number of (token, choice) pairs, which bounds the tokens.
 size_t mx_moe_ws_bytes(int64_t pairs, int64_t hidden, int64_t inter) {
     if (pairs <= 0 || hidden <= 0 || inter <= 0) return 0;
-    const size_t tokens = (size_t)std::min<int64_t>(pairs, kMaxT), blocks = (size_t)(hidden + 63) / 64;
+    const size_t tokens = (size_t)std::min<int64_t>(pairs, kMaxT), blocks = (size_t)(hidden + kTallRows - 1) / kTallRows;
     return align256(kMaxT * 4) + align256(kMaxE * 4) + align256(kMaxE * tokens * 2) +
-           align256((size_t)pairs * inter * 4) + align256(blocks * 4) + blocks * 4 * tokens * 64 * 4;
+           align256((size_t)pairs * inter * 4) + align256(blocks * 4) + blocks * kTallTiles * tokens * kTallRows * 4;
 }
 
 hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStream_t stream) {
@@ -567,7 +566,7 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     ws += align256((size_t)kMaxE * a.T * 2);
     a.h = reinterpret_cast<__bf16 *>(ws);
     ws += align256((size_t)a.T * a.k * a.I * 4);
-    const int blocks = (a.H + 63) / 64;
+    const int blocks = (a.H + kTallRows - 1) / kTallRows;
     a.arrived = reinterpret_cast<uint32_t *>(ws);
     a.parts = reinterpret_cast<float *>(ws + align256((size_t)blocks * 4));
     a.pair_slots = a.T * a.k < a.E ? 1 : 0;
@@ -581,8 +580,8 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     if (p.logits_bf16) launch_up<true>(a, stream);
     else launch_up<false>(a, stream);
     if (tall) {
-        if (p.y_bf16) launch_down<__bf16, 4>(a, blocks * 4, stream);
-        else launch_down<float, 4>(a, blocks * 4, stream);
+        if (p.y_bf16) launch_down<__bf16, kTallTiles>(a, blocks * kTallTiles, stream);
+        else launch_down<float, kTallTiles>(a, blocks * kTallTiles, stream);
     } else {
         if (p.y_bf16) launch_down<__bf16, 1>(a, a.H / 16, stream);
         else launch_down<float, 1>(a, a.H / 16, stream);
