@@ -291,7 +291,8 @@ def _check_moe(nv, case, e, k, renorm, out="bf16"):
 MOE_CASES = [(1, 8, 2, 64, 32), (1, 1, 1, 32, 32), (1, 64, 8, 512, 96), (2, 5, 5, 96, 160), (3, 16, 3, 544, 64),
              (7, 4, 2, 128, 544), (16, 8, 2, 256, 64), (17, 130, 4, 64, 32), (33, 12, 3, 160, 96), (64, 8, 4, 96, 64),
              (64, 512, 16, 32, 32), (50, 3, 1, 1056, 32),
-             (64, 2, 2, 160, 1056), (12, 3, 2, 96, 544), (40, 8, 4, 4128, 96), (2, 1, 1, 32, 512)]
+             (64, 2, 2, 160, 1056), (12, 3, 2, 96, 544), (5, 4, 2, 1536, 416), (3, 6, 2, 2048, 288),
+             (9, 4, 2, 832, 160), (40, 8, 4, 4128, 96), (2, 1, 1, 32, 512)]
 
 
 @pytest.mark.parametrize("renorm", [True, False])
