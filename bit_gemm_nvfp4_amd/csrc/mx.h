@@ -47,18 +47,9 @@ __device__ __forceinline__ MxGroup load_mx_group(const uint8_t *codes, const uin
     return r;
 }
 
-// The last, partial group (nblk < kGroupBlocks blocks are left): blocks past the row's end read as zero
-// codes with scale 2^-127.
-__device__ __forceinline__ MxGroup load_mx_tail(const uint8_t *codes, const uint8_t *scales, int grp, int lg,
-                                                int nblk) {
-    MxGroup r;
-    const uint8_t *cp = codes + (int64_t)grp * (kGroup / 2) + lg * 16;
+// The scale bytes of a partial group (nblk < kGroupBlocks blocks are left); those past the row's end are 0.
+__device__ __forceinline__ u32x4 load_mx_tail_scales(const uint8_t *scales, int grp, int nblk) {
     const uint8_t *sp = scales + (int64_t)grp * kGroupBlocks;
-#pragma unroll
-    for (int i = 0; i < kGroupChunks; i++) {
-        r.c[i] = u32x4{0, 0, 0, 0};
-        if (i * 4 + lg < nblk) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
-    }
     uint32_t s[4] = {0, 0, 0, 0};
     for (int b = 0; b < nblk; b++) {
         const uint32_t v = sp[b];
@@ -66,7 +57,21 @@ __device__ __forceinline__ MxGroup load_mx_tail(const uint8_t *codes, const uint
         for (int i = 0; i < 4; i++)
             if (b / 4 == i) s[i] |= v << (8 * (b % 4));
     }
-    r.s = u32x4{s[0], s[1], s[2], s[3]};
+    return u32x4{s[0], s[1], s[2], s[3]};
+}
+
+// The last, partial group (nblk < kGroupBlocks blocks are left): blocks past the row's end read as zero
+// codes with scale 2^-127.
+__device__ __forceinline__ MxGroup load_mx_tail(const uint8_t *codes, const uint8_t *scales, int grp, int lg,
+                                                int nblk) {
+    MxGroup r;
+    const uint8_t *cp = codes + (int64_t)grp * (kGroup / 2) + lg * 16;
+#pragma unroll
+    for (int i = 0; i < kGroupChunks; i++) {
+        r.c[i] = u32x4{0, 0, 0, 0};
+        if (i * 4 + lg < nblk) r.c[i] = *reinterpret_cast<const u32x4 *>(cp + i * 64);
+    }
+    r.s = load_mx_tail_scales(scales, grp, nblk);
     return r;
 }
 
@@ -114,18 +119,38 @@ __device__ __forceinline__ Bf16Group load_bf16_group(const __bf16 *row, int grp,
     return r;
 }
 
-// acc[t] += W[t] . a over a group: the lane's W blocks are expanded exactly to bf16, sixteen instructions a tile.
+// buffer_rsrc with its words forced into scalar registers: a base formed by vector 64-bit arithmetic, though
+// the same in every lane, would have each load wrapped in a loop over the lanes' values.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const uint8_t *base, uint32_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return buffer_rsrc(reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo),
+                       (uint32_t)__builtin_amdgcn_readfirstlane(bytes));
+}
+
+// acc[t] += W[t] . a over chunk i of a group: the lane's W blocks are expanded exactly to bf16, four instructions
+// a tile.  s: the chunk's word of scale bytes of each tile.
+template <int RT>
+__device__ __forceinline__ void chunk_product(const MxGroup (&w)[RT], const uint32_t (&s)[RT], const Bf16Group &a, int i,
+                                              int lg, f32x4 (&acc)[RT]) {
+#pragma unroll
+    for (int t = 0; t < RT; t++) {
+        const float f = scale_operand(s[t], lg);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            acc[t] = mfma_bf16(fp4_to_bf16x8(w[t].c[i][j], f), __builtin_bit_cast(bf16x8, a.v[i][j]), acc[t]);
+    }
+}
+
 template <int RT>
 __device__ __forceinline__ void group_product(const MxGroup (&w)[RT], const Bf16Group &a, int lg, f32x4 (&acc)[RT]) {
 #pragma unroll
-    for (int i = 0; i < kGroupChunks; i++)
+    for (int i = 0; i < kGroupChunks; i++) {
+        uint32_t s[RT];
 #pragma unroll
-        for (int t = 0; t < RT; t++) {
-            const float s = scale_operand(w[t].s[i], lg);
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                acc[t] = mfma_bf16(fp4_to_bf16x8(w[t].c[i][j], s), __builtin_bit_cast(bf16x8, a.v[i][j]), acc[t]);
-        }
+        for (int t = 0; t < RT; t++) s[t] = w[t].s[i];
+        chunk_product<RT>(w, s, a, i, lg, acc);
+    }
 }
 
 // Host side ---------------------------------------------------------------------------------------

@@ -198,15 +198,6 @@ __device__ __forceinline__ u32x4 load_scale_window(const uint8_t *row, int windo
     return u32x4{s[0], s[1], s[2], s[3]};
 }
 
-// buffer_rsrc with its words forced into scalar registers: a base formed by vector 64-bit arithmetic, though
-// the same in every lane, would have each load wrapped in a loop over the lanes' values.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const uint8_t *base, uint32_t bytes) {
-    const uint64_t b = reinterpret_cast<uint64_t>(base);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
-    return buffer_rsrc(reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo),
-                       (uint32_t)__builtin_amdgcn_readfirstlane(bytes));
-}
-
 struct MxTileArgs {
     const uint8_t *a;  // MXFP4 codes or bf16 rows
     const uint8_t *ascales;

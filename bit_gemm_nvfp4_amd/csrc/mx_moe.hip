@@ -217,18 +217,51 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
     };
     // the wave's items: groups wave, wave + kUpWaves, ... of tile 0, 1, ...
     const int gw = wave < groups ? (groups - wave + kUpWaves - 1) / kUpWaves : 0, items = ntile * gw;
-    auto load_w = [&](int it) -> Pair {
-        const int tile = XREG ? it : it / gw, g = XREG ? wave : wave + it % gw * kUpWaves;
-        const int64_t row = (int64_t)e * 2 * a.I + (tile0 + tile) * 16 + r;
-        const uint8_t *gc = a.gu_codes + row * (a.H / 2), *gs = a.gu_scales + row * kb;
-        const uint8_t *uc = gc + (int64_t)a.I * (a.H / 2), *us = gs + (int64_t)a.I * kb;
-        if (g < full) return Pair{{load_mx_group(gc, gs, g, lg), load_mx_group(uc, us, g, lg)}};
-        return Pair{{load_mx_tail(gc, gs, g, lg, tail), load_mx_tail(uc, us, g, lg, tail)}};
+    // An item's codes are read through buffers of its sixteen gate and its sixteen up rows, so that blocks past a
+    // row's end and items past the last one load nothing, without a branch.
+    struct Item {
+        __amdgpu_buffer_rsrc_t rsrc[2];
+        int soff, left;  // of the group: byte offset, and the blocks from its start to the row's end
+    };
+    const int row_bytes = a.H / 2;
+    const uint32_t voff = (uint32_t)(r * row_bytes + lg * 16);
+    auto item_row = [&](int it) -> int64_t { return (int64_t)e * 2 * a.I + (tile0 + (XREG ? it : it / gw)) * 16; };
+    auto item_group = [&](int it) -> int { return XREG ? wave : wave + it % gw * kUpWaves; };
+    auto item_of = [&](int it) -> Item {
+        if (it >= items) return Item{{uniform_rsrc(a.gu_codes, 0), uniform_rsrc(a.gu_codes, 0)}, 0, 0};
+        const uint8_t *gc = a.gu_codes + item_row(it) * row_bytes;
+        const int g = item_group(it);
+        return Item{{uniform_rsrc(gc, 16 * row_bytes), uniform_rsrc(gc + (int64_t)a.I * row_bytes, 16 * row_bytes)},
+                    g * (kGroup / 2), kb - g * kGroupBlocks};
+    };
+    auto load_scales = [&](int it, Pair &w) {
+        if (it >= items) return;
+        const int g = item_group(it);
+        const uint8_t *gs = a.gu_scales + (item_row(it) + r) * kb, *us = gs + (int64_t)a.I * kb;
+        if (g < full) {
+            w.t[0].s = *reinterpret_cast<const u32x4_u *>(gs + g * kGroupBlocks);
+            w.t[1].s = *reinterpret_cast<const u32x4_u *>(us + g * kGroupBlocks);
+        } else {
+            w.t[0].s = load_mx_tail_scales(gs, g, tail);
+            w.t[1].s = load_mx_tail_scales(us, g, tail);
+        }
+    };
+    auto load_chunk = [&](const Item &m, int i, Pair &w) {
+        const uint32_t o = i * 4 + lg < m.left ? voff + i * 64 : kOffsetPastRange;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            w.t[j].c[i] = __builtin_amdgcn_raw_buffer_load_b128(m.rsrc[j], (int)o, m.soff, 0);
+    };
+    auto load_w = [&](int it, Pair &w) {
+        const Item m = item_of(it);
+#pragma unroll
+        for (int i = 0; i < kGroupChunks; i++) load_chunk(m, i, w);
+        load_scales(it, w);
     };
     // two items in flight while the tokens are looked up
-    Pair w{}, w1{};
-    if (items > 0) w = load_w(0);
-    if (items > 1) w1 = load_w(1);
+    Pair w[2] = {};
+    load_w(0, w[0]);
+    load_w(1, w[1]);
 
     // the tokens that chose e
     for (int t = wave; t < a.T; t += kUpWaves) {
@@ -264,28 +297,38 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
         Bf16Group x;
         if (XREG && gw > 0) x = load_x(wave);
         if (q > 0) {
-            if (items > 0) w = load_w(0);
-            if (items > 1) w1 = load_w(1);
+            load_w(0, w[0]);
+            load_w(1, w[1]);
         }
+        // One item: its products, each chunk's registers taking the chunk of the item after next as they get free.
+        auto step = [&](Pair &p, int it, f32x4(&acc)[2]) {
+            if constexpr (!XREG) x = load_x(item_group(it));
+            const u32x4 s0 = p.t[0].s, s1 = p.t[1].s;
+            const Item m = item_of(it + 2);
+            load_scales(it + 2, p);
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; i++) {
+                chunk_product<2>(p.t, {s0[i], s1[i]}, x, i, lg, acc);
+                __builtin_amdgcn_sched_barrier(0);
+                load_chunk(m, i, p);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
         int it = 0;
         for (int c0 = 0; c0 < ntile; c0 += kUpTiles) {
             f32x4 acc[kUpTiles][2] = {};
 #pragma unroll
             for (int t = 0; t < kUpTiles; t++) {
                 if (c0 + t >= ntile) break;
-                for (int j = 0; j < gw; j++, it++) {
-                    if constexpr (!XREG) x = load_x(wave + j * kUpWaves);
-                    if (it + 2 < items) {
-                        // loads return in order: the activations, which come from L2, go ahead
-                        __builtin_amdgcn_sched_barrier(0);
-                        const Pair w2 = load_w(it + 2);
-                        __builtin_amdgcn_sched_barrier(0);
-                        group_product<2>(w.t, x, lg, acc[t]);
-                        w = w1;
-                        w1 = w2;
-                    } else {
-                        group_product<2>(w.t, x, lg, acc[t]);
-                        w = w1;
+                if constexpr (XREG) {
+                    static_assert(kUpTiles % 2 == 0, "item it is in w[it % 2]");
+                    if (gw > 0) step(w[t % 2], it++, acc[t]);
+                } else {
+                    for (int j = 0; j < gw; j++, it++) {
+                        step(w[0], it, acc[t]);
+                        const Pair next = w[1];
+                        w[1] = w[0];
+                        w[0] = next;
                     }
                 }
             }
