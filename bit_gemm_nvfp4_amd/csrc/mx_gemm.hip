@@ -7,9 +7,12 @@
 // k_mx_skinny (M <= 16): bound by streaming W.  A wave reads 16 W rows straight into registers in the
 //   operand layout (MxGroup), the waves of a workgroup split K and add their partial tiles in LDS in
 //   wave order.  MXFP4 activations take v_mfma_scale_f32_16x16x128; bf16 activations take
-//   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element).
+//   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element).  1 x 12288 x 4096
+//   W4A16: 7.8 us, 3.4 TB/s of W; 13 x 4096 x 12288: 15 us, where each workgroup's reading of all of A through L2
+//   (320 KB beside 105 KB of W) takes longer than the stream of W.
 // k_mx_tile (M > 16): BM x BN output tile per workgroup, operands through LDS by direct-to-LDS loads,
-//   v_mfma_scale_f32_32x32x64 for MXFP4 activations, v_mfma_f32_32x32x16_bf16 for bf16 ones.
+//   v_mfma_scale_f32_32x32x64 for MXFP4 activations, v_mfma_f32_32x32x16_bf16 for bf16 ones.  4096 x 12288 x
+//   4096: W4A4 111 us, 3.7 PFLOP/s; W4A16 327 us, 1.26 PFLOP/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -296,7 +299,10 @@ __device__ __forceinline__ void order_step() {
 // quarter read while the matrix instructions of this one issue.  The barrier stands before the last quarter,
 // whose operands are then in registers: behind it stage s + 1 is complete, so the first operands of step s + 1
 // are read under the last quarter's instructions, and stage s may be overwritten.
-// W4A16 512 x 4096 x 12288 in quarters: 60.7 us; W4A4 512 x 12288 x 4096: 25.0 us.
+// W4A16 512 x 4096 x 12288 in quarters: 60.7 us (59.1 in whole steps); W4A4 512 x 12288 x 4096: 25.0 us (23.9).
+// What bounds the largest W4A4 tile: a step of 256 columns takes 1.92 us, 1.30 us of them matrix instructions (the
+// same loop without anything else) and 1.50 us with the LDS reads; the rest goes to the direct-to-LDS loads, which
+// share the LDS with the reads, and the wait at the barrier.
 template <class T, class OT, bool SPLIT>
 __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(MxTileArgs p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];

@@ -104,8 +104,8 @@ nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
  *           their p; -1 and 0 where a row has fewer
  * H and I are multiples of 32.  Sums are fp32; between the two products the activations are carried as
  * two bf16 planes (their value to 2^-17).  The result does not depend on the order of execution.
- * Errors: NVFP4_ERR_SHAPE for tokens > 64, experts > 512, top_k > 16 or operands that disagree;
- * NVFP4_ERR_ARG for top_k < 1, top_k > experts or a bad renormalize; NVFP4_ERR_WORKSPACE for less than
+ * Errors: NVFP4_ERR_SHAPE for tokens > 64, experts > 512, top_k > 16, H or I above 2^22, or operands that
+ * disagree; NVFP4_ERR_ARG for top_k < 1, top_k > experts or a bad renormalize; NVFP4_ERR_WORKSPACE for less than
  * mxfp4_workspace_size(MXFP4_OP_MOE, tokens * top_k, H, I) bytes (16-byte aligned).
  */
 nvfp4_status mxfp4_moe(const void *x, int64_t tokens, int64_t ld_x, const void *logits, nvfp4_dtype logits_dtype,
