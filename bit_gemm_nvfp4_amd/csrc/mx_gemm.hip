@@ -7,9 +7,9 @@
 // k_mx_skinny (M <= 16): bound by streaming W.  A wave reads 16 W rows straight into registers in the
 //   operand layout (MxGroup), the waves of a workgroup split K and add their partial tiles in LDS in
 //   wave order.  MXFP4 activations take v_mfma_scale_f32_16x16x128; bf16 activations take
-//   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element).  1 x 12288 x 4096
-//   W4A16: 7.8 us, 3.4 TB/s of W; 13 x 4096 x 12288: 15 us, where each workgroup's reading of all of A through L2
-//   (320 KB beside 105 KB of W) takes longer than the stream of W.
+//   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element), with A staged in
+//   LDS.  Calls in a row, W4A16: 1 x 12288 x 4096 7.5 us, 3.6 TB/s of W; 13 x 4096 x 12288 11.8 us, where each
+//   workgroup's reading of all of A through L2 (320 KB beside 105 KB of W) comes on top of the stream of W.
 // k_mx_tile (M > 16): BM x BN output tile per workgroup, operands through LDS by direct-to-LDS loads,
 //   v_mfma_scale_f32_32x32x64 for MXFP4 activations, v_mfma_f32_32x32x16_bf16 for bf16 ones.  4096 x 12288 x
 //   4096: W4A4 111 us, 3.7 PFLOP/s; W4A16 327 us, 1.26 PFLOP/s.
@@ -36,21 +36,31 @@ __device__ __forceinline__ void store_out(OT *p, float v) {
 // -------------------------------------------------------------------------------------------------
 // M <= 16
 // -------------------------------------------------------------------------------------------------
+// Bytes between two staged rows of A: sixteen rows start in different banks.
+constexpr int kStageRow = kGroup * 2 + 16;
+
 // RT tiles of 16 W rows per wave share its activation operands.  The W groups of a wave are wave, wave +
-// waves, ...; the next one's loads are issued before the current one's products.
-template <int RT, bool A_MX, class OT>
+// waves, ....
+//
+// MR > 0: bf16 activations, at most MR rows.  A wave stages the rows that a group needs in LDS, a direct-to-LDS load
+// of 1 KiB each, one group ahead, with the W groups of the next two in flight.  Read straight in the operand
+// layout, each load's 64 lanes would ask for 16-byte pieces of sixteen rows, which the address unit takes piece by
+// piece (13 x 4096 x 12288 15.5 -> 11.8 us, 4 rows 10.9 -> 9.0 us).
+// MR = 0: MXFP4 activations, a quarter of that, read straight; the next W group's loads are issued before the
+// current one's products.  The other loop is no faster there (13 x 4096 x 12288 8.9 us, with it 9.8).
+template <int RT, int MR, class OT>
 __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A, int64_t lda,
                                                    const uint8_t *__restrict__ acodes,
                                                    const uint8_t *__restrict__ ascales, int M,
                                                    const uint8_t *__restrict__ wcodes,
-                                                   const uint8_t *__restrict__ wscales, int64_t N, int K,
+                                                   const uint8_t *__restrict__ wscales, int64_t N, int K, int stages,
                                                    OT *__restrict__ C, int64_t ldc) {
-    extern __shared__ float red[];  // [waves][RT][256]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    extern __shared__ __align__(16) float red[];  // [waves][RT][256], then [waves][stages][MR][kStageRow] bytes
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
     const int kb = K / kMxBlock, full = K / kGroup, tail = kb - full * kGroupBlocks;
-    // rows past N or M repeat the last one; their results are not stored
+    // rows past N or M repeat the last one, or are zeros; their results are not stored
     const uint8_t *wc[RT], *ws[RT];
 #pragma unroll
     for (int i = 0; i < RT; i++) {
@@ -58,13 +68,11 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A,
         wc[i] = wcodes + row * (K / 2);
         ws[i] = wscales + row * kb;
     }
-    const int64_t arow = min(r, M - 1);
-    const uint8_t *ac = acodes + arow * (K / 2), *as = ascales + arow * kb;
-    const __bf16 *ar = A + arow * lda;
-    using AGroup = std::conditional_t<A_MX, MxGroup, Bf16Group>;
     f32x4 acc[RT] = {};
-    auto product = [&](const MxGroup (&w)[RT], const AGroup &a) {
-        if constexpr (A_MX) {
+    if constexpr (MR == 0) {
+        const int64_t arow = min(r, M - 1);
+        const uint8_t *ac = acodes + arow * (K / 2), *as = ascales + arow * kb;
+        auto product = [&](const MxGroup (&w)[RT], const MxGroup &a) {
 #pragma unroll
             for (int i = 0; i < kGroupChunks; i++)
 #pragma unroll
@@ -72,40 +80,137 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A,
                     acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                         fp4_operand(w[t].c[i]), fp4_operand(a.c[i]), acc[t], 4, 4, 0, (int)(w[t].s[i] >> (8 * lg)), 0,
                         (int)(a.s[i] >> (8 * lg)));
-        } else {
-            group_product<RT>(w, a, lg, acc);
+        };
+        MxGroup w[RT];
+        if (wave < full) {
+#pragma unroll
+            for (int i = 0; i < RT; i++) w[i] = load_mx_group(wc[i], ws[i], wave, lg);
+            int g = wave;
+            for (; g + waves < full; g += waves) {
+                // loads return in order: the activations, which come from L2, go ahead of the next W group
+                const MxGroup a = load_mx_group(ac, as, g, lg);
+                __builtin_amdgcn_sched_barrier(0);
+                MxGroup next[RT];
+#pragma unroll
+                for (int i = 0; i < RT; i++) next[i] = load_mx_group(wc[i], ws[i], g + waves, lg);
+                __builtin_amdgcn_sched_barrier(0);
+                product(w, a);
+#pragma unroll
+                for (int i = 0; i < RT; i++) w[i] = next[i];
+            }
+            product(w, load_mx_group(ac, as, g, lg));
         }
-    };
-    auto load_a = [&](int g) -> AGroup {
-        if constexpr (A_MX) return load_mx_group(ac, as, g, lg);
-        else return load_bf16_group<false>(ar, g, lg);
-    };
-    MxGroup w[RT];
-    if (wave < full) {
+        if (tail > 0 && full % waves == wave) {
+            const MxGroup a = load_mx_tail(ac, as, full, lg, tail);
 #pragma unroll
-        for (int i = 0; i < RT; i++) w[i] = load_mx_group(wc[i], ws[i], wave, lg);
-        int g = wave;
-        for (; g + waves < full; g += waves) {
-            // loads return in order: the activations, which come from L2, go ahead of the next W group
-            const AGroup a = load_a(g);
-            __builtin_amdgcn_sched_barrier(0);
-            MxGroup next[RT];
-#pragma unroll
-            for (int i = 0; i < RT; i++) next[i] = load_mx_group(wc[i], ws[i], g + waves, lg);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < RT; i++) w[i] = load_mx_tail(wc[i], ws[i], full, lg, tail);
             product(w, a);
-#pragma unroll
-            for (int i = 0; i < RT; i++) w[i] = next[i];
         }
-        product(w, load_a(g));
-    }
-    if (tail > 0 && full % waves == wave) {
-        AGroup a;
-        if constexpr (A_MX) a = load_mx_tail(ac, as, full, lg, tail);
-        else a = load_bf16_group<true>(ar, full, lg, tail);
+    } else {
+        // Codes of full groups come through a buffer of the workgroup's rows; those of groups past the last full
+        // one from an empty one.
+        const int row_bytes = K / 2, rows = (int)min((int64_t)16 * RT, N - n0);
+        const uint32_t voff = (uint32_t)(r * row_bytes + lg * 16);
+        auto load_codes = [&](MxGroup (&w)[RT], int g, int i) {
+            const __amdgpu_buffer_rsrc_t rw =
+                uniform_rsrc(wcodes + n0 * row_bytes, g < full ? (uint32_t)(rows * row_bytes) : 0u);
 #pragma unroll
-        for (int i = 0; i < RT; i++) w[i] = load_mx_tail(wc[i], ws[i], full, lg, tail);
-        product(w, a);
+            for (int t = 0; t < RT; t++)
+                w[t].c[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(voff + i * 64),
+                                                                  g * (kGroup / 2) + t * 16 * row_bytes, 0);
+        };
+        auto load_scales = [&](MxGroup (&w)[RT], int g) {
+#pragma unroll
+            for (int t = 0; t < RT; t++)
+                w[t].s = *reinterpret_cast<const u32x4_u *>(ws[t] + (int64_t)min(g, full - 1) * kGroupBlocks);
+        };
+        uint8_t *mine = reinterpret_cast<uint8_t *>(red + waves * (RT * 256)) + wave * (stages * MR * kStageRow);
+        auto stage = [&](int g, int b) {  // rows past M and columns past K become zeros
+            const int bytes = min(kGroup, K - g * kGroup) * 2;
+#pragma unroll
+            for (int m = 0; m < MR; m++) {
+                const __bf16 *row = A + min(m, M - 1) * lda + (int64_t)g * kGroup;
+                load_to_lds16(uniform_rsrc(reinterpret_cast<const uint8_t *>(row), m < M && bytes > 0 ? bytes : 0),
+                              mine + (b * MR + m) * kStageRow, lane * 16, 0);
+            }
+            // what arrived() counts as behind these loads stays behind them
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // all but the last n loads have arrived, those into LDS among them
+        auto arrived = [](auto n) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(n, 15));
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto product = [&](const MxGroup (&w)[RT], int b, int i) {
+            const uint8_t *p = mine + (b * MR + r % MR) * kStageRow + lg * 64 + i * 256;
+            Bf16Group a;
+            uint32_t s[RT];
+#pragma unroll
+            for (int j = 0; j < 4; j++) a.v[i][j] = *reinterpret_cast<const u32x4 *>(p + j * 16);
+#pragma unroll
+            for (int t = 0; t < RT; t++) s[t] = w[t].s[i];
+            chunk_product<RT>(w, s, a, i, lg, acc);
+        };
+        // behind the rows of a group come at least the loads of one W group
+        constexpr std::integral_constant<int, RT * (kGroupChunks + 1)> behind;
+        // One group, with the next one's rows of A behind it, and each chunk's registers taking the chunk of the W
+        // group after next as they get free.
+        auto step = [&](MxGroup (&p)[RT], int g, int b) {
+            arrived(behind);
+            stage(min(g + waves, full), b ^ 1);
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; i++) {
+                product(p, b, i);
+                __builtin_amdgcn_sched_barrier(0);
+                load_codes(p, g + 2 * waves, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            load_scales(p, g + 2 * waves);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto load_w = [&](MxGroup (&p)[RT], int g) {  // in the order of use
+            load_scales(p, g);
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; i++) {
+                __builtin_amdgcn_sched_barrier(0);
+                load_codes(p, g, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        MxGroup w[2][RT];
+        if (wave < full) {
+            stage(wave, 0);
+            load_w(w[0], wave);
+            int g = wave;
+            if (g + waves < full) {
+                load_w(w[1], g + waves);
+                // (two steps in one block: with a way out between them the compiler moves loads of one to the other)
+                do {
+                    step(w[0], g, 0);
+                    step(w[1], g + waves, 1);
+                    g += 2 * waves;
+                } while (g + waves < full);
+            }
+            if (g < full) {
+                arrived(behind);
+#pragma unroll
+                for (int i = 0; i < kGroupChunks; i++) product(w[0], 0, i);
+            }
+        }
+        if (tail > 0 && full % waves == wave) {
+            __builtin_amdgcn_sched_barrier(0);
+            stage(full, 0);
+#pragma unroll
+            for (int i = 0; i < RT; i++) w[0][i] = load_mx_tail(wc[i], ws[i], full, lg, tail);
+            arrived(std::integral_constant<int, 0>());
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; i++) product(w[0], 0, i);
+        }
+        // no load may be in flight into the LDS of a workgroup that has ended
+        arrived(std::integral_constant<int, 0>());
     }
 #pragma unroll
     for (int i = 0; i < RT; i++) *reinterpret_cast<f32x4 *>(&red[(wave * RT + i) * 256 + lane * 4]) = acc[i];
@@ -729,35 +834,39 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
     }
 }
 
-template <int RT, bool A_MX, class OT>
+template <int RT, int MR, class OT>
 void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
-                     int64_t ldc, int waves, hipStream_t stream) {
+                     int64_t ldc, int waves, int stages, hipStream_t stream) {
     const unsigned wgs = (unsigned)((w->rows + 16 * RT - 1) / (16 * RT));
-    hipLaunchKernelGGL((k_mx_skinny<RT, A_MX, OT>), dim3(wgs), dim3(64 * waves), (size_t)waves * RT * 1024, stream,
-                       reinterpret_cast<const __bf16 *>(a_bf16), lda, A_MX ? a_q->codes : nullptr,
-                       A_MX ? a_q->scales : nullptr, (int)M, w->codes, w->scales, w->rows, (int)w->cols, c, ldc);
+    const size_t lds = (size_t)waves * (RT * 1024 + stages * MR * kStageRow);
+    hipLaunchKernelGGL((k_mx_skinny<RT, MR, OT>), dim3(wgs), dim3(64 * waves), lds, stream,
+                       reinterpret_cast<const __bf16 *>(a_bf16), lda, a_q ? a_q->codes : nullptr,
+                       a_q ? a_q->scales : nullptr, (int)M, w->codes, w->scales, w->rows, (int)w->cols, stages, c, ldc);
 }
 
 // W row tiles per workgroup and its waves.  Every workgroup reads all of A through L2 (16 rows of bf16 are 3.8
 // times a tile of W), so tiles share it, as many as spread over the CUs in one round, up to three (four
-// spill).  Measured, us (K = 4096 unless said), the pick marked:
-//   bf16  16 x 12288: 1 tile 17.0, 2 tiles 15.2, 3 tiles 11.1 *, 4 tiles 12.0;  1 x 12288: 9.7, 10.0, 8.1 *, 9.0
-//   bf16  16 x 6000:  1 tile 11.9, 2 tiles 8.7 *, 3 tiles 10.0;   8 x 8192: 9.1, 7.4 *, 8.5
-//   bf16  16 x 4096:  1 tile 7.3 *, 2 tiles 8.5;   13 x 4096, K = 12288: 15.1 *, 18.3
-//   bf16  16 x 12288, K = 12288: 1 tile 45.4, 2 tiles 39.7, 3 tiles 27.5 *, 4 tiles 37.0
-//   MXFP4 16 x 12288: 9.6, 10.0, 8.2 *, 9.2;  1 x 12288: 7.2, 8.0, 7.1 *, 7.8;  16 x 6000: 7.0, 6.2 *, 7.3
-// Waves split K: 8 with three tiles (2 and 4 waves 11.3, 11.4 against 11.1), else 4 (8 x 8192: 2, 4, 8 waves 7.3,
-// 7.4, 7.6).
-template <bool A_MX, class OT>
+// spill).  Measured, us (K = 4096 unless said), with 1, 2 and 3 tiles, the pick marked:
+//   bf16  1 x 12288: 9.0, 10.0, 7.5 *;  16 x 12288: 13.9, 12.9, 9.6 *;  16 x 12288, K = 12288: 35.8, 32.9, 24.5 *
+//   bf16  16 x 6000: 8.9, 6.9 *, 8.2;  8 x 8192: 7.9, 6.9 *, 7.3
+//   bf16  16 x 4096: 5.4 *, 6.6, 8.0;  13 x 4096, K = 12288: 11.8 *, 15.9, 20.7
+//   MXFP4 1 x 12288: 7.4, 8.0, 7.0 *;  16 x 12288: 9.6, 10.0, 8.2 *;  16 x 6000: 7.0, 6.2 *, 7.3
+//   MXFP4 16 x 4096: 4.8 *, 6.0, 7.2;  13 x 4096, K = 12288: 8.9 *, 12.3, 15.6
+// Waves split K.  MXFP4: 8 with three tiles (2 and 4 waves 11.3, 11.4 against 11.1), else 4 (8 x 8192: 2, 4, 8 waves
+// 7.3, 7.4, 7.6).  bf16, up to 8 rows: 8 where three tiles make one round (1 x 12288 8.3, with 4 8.8), else 4 (1 x
+// 50000 29.5, with 8 34.8).  bf16, 16 rows: 8 where one stage of A per wave is enough (16 x 4096 5.8, with 4 6.3);
+// two fit in LDS only four times.
+template <int MR, class OT>
 void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
                    int64_t ldc, int num_cus, hipStream_t stream) {
     const int64_t tiles = (w->rows + 15) / 16, groups = (w->cols + kGroup - 1) / kGroup;
     const int64_t share = (tiles + num_cus - 1) / num_cus;
-    int waves = share >= 3 ? 8 : 4;
+    int waves = (MR == 0 ? share >= 3 : MR == 16 ? groups <= 8 : share == 3) ? 8 : 4;
     while (waves > 1 && waves / 2 >= groups) waves /= 2;  // no more waves than groups to share out
-    if (share >= 3) launch_skinny_t<3, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
-    else if (share == 2) launch_skinny_t<2, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
-    else launch_skinny_t<1, A_MX, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stream);
+    const int stages = groups > waves ? 2 : 1;
+    if (share >= 3) launch_skinny_t<3, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, stream);
+    else if (share == 2) launch_skinny_t<2, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, stream);
+    else launch_skinny_t<1, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, stream);
 }
 
 template <class OT>
@@ -768,8 +877,10 @@ hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t
         const int64_t blocks = std::min<int64_t>((M * w->rows + 255) / 256, 4096);
         hipLaunchKernelGGL(k_mx_zero<OT>, dim3((unsigned)blocks), dim3(256), 0, stream, c, M, w->rows, ldc);
     } else if (M <= kSkinnyMaxM) {
-        if (a_q) launch_skinny<true>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
-        else launch_skinny<false>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        if (a_q) launch_skinny<0>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        else if (M <= 4) launch_skinny<4>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        else if (M <= 8) launch_skinny<8>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        else launch_skinny<16>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
     } else {
         launch_tiled(a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     }
