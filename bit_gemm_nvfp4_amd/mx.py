@@ -107,7 +107,10 @@ def _opt(t: torch.Tensor | None, device: torch.device, name: str, dtype: torch.d
 
 
 def _nbytes(t: torch.Tensor | None) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    if t is None:
+        return 0
+    assert t.is_contiguous(), "workspace: a dense tensor is required"
+    return t.numel() * t.element_size()
 
 
 def _out(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype, device, what: str):

@@ -458,3 +458,28 @@ def test_int64_offsets(nv):
     far[:, :k] = 1
     assert bool((nv.mx_gemm(far[:, :k], w, dtype=torch.bfloat16)[:, rows - 1] == k).all())
     assert bool((nv.mx_dequantize(nv.mx_quantize(far[:, :k])) == 1).all())
+
+
+# one token over many experts, and two tokens per expert (the tall down product), H beyond the register form
+@pytest.mark.parametrize("case", [(1, 96, 4096, 12288), (64, 32, 8192, 16896)], ids=lambda s: "x".join(map(str, s)))
+def test_moe_int64_offsets(nv, case):
+    t, e, h, i = case
+
+    def zeros(rows, cols):
+        return nv.MXFP4Tensor(torch.zeros((rows, cols // 2), dtype=torch.uint8, device=DEV),
+                              torch.full((rows, cols // 32), 127, dtype=torch.uint8, device=DEV))
+    gu, dn = zeros(e * 2 * i, h), zeros(e * h, i)
+    assert gu.codes.numel() > 2 ** 31 and dn.codes.numel() > 2 ** 31
+    # the last expert: inner element i - 1 is silu(1) * 1, output element h - 1 takes it
+    gu.codes[(e - 1) * 2 * i + i - 1, 0] = 0x02
+    gu.codes[e * 2 * i - 1, 0] = 0x02
+    dn.codes[e * h - 1, i // 2 - 1] = 0x20
+    x = torch.zeros((t, h), dtype=torch.bfloat16, device=DEV)
+    x[:, 0] = 1
+    logits = torch.zeros((t, e), device=DEV)
+    logits[:, e - 1] = 1
+    y = nv.mx_moe(x, logits, gu, dn, 1, dtype=torch.float32).double().cpu().numpy()
+    want = 1 / (1 + np.exp(-1.0))
+    # two planes of h (2^-17) and a few fp32 roundings (exp, quotient, product, sums with zeros)
+    assert (np.abs(y[:, h - 1] - want) <= want * (2.0 ** -17 + 8 * 2.0 ** -24)).all()
+    assert (y[:, :h - 1] == 0).all()
