@@ -168,5 +168,8 @@ def test_binding_refusals(nv):
         t.c()  # 64 columns need two scale bytes per row (and a device tensor)
     with pytest.raises(AssertionError):
         nv.mx_quantize(torch.zeros((4, 64)))  # host tensor
+    from bit_gemm_nvfp4_amd import mx
+    with pytest.raises(AssertionError):
+        mx._nbytes(torch.zeros(1, dtype=torch.uint8).expand(4096))  # a workspace that is not what it seems
     with pytest.raises(AssertionError):
         nv.mx_gemm(torch.zeros((4, 64)), t)  # fp32 activations

@@ -146,7 +146,11 @@ def _acts(nv, rng, m, k, act):
 
 
 GEMM_SHAPES = [(1, 1, 32), (1, 4099, 4096), (2, 48, 96), (3, 17, 480), (5, 300, 512), (8, 64, 544), (13, 1000, 1056),
-               (16, 16, 12288), (2, 5000, 608), (15, 8200, 544), (16, 17001, 160), (4, 12300, 6176), (17, 33, 160), (31, 129, 2048), (33, 200, 608), (48, 77, 1024), (64, 512, 96),
+               (16, 16, 12288), (2, 5000, 608), (15, 8200, 544), (16, 17001, 160), (4, 12300, 6176),
+               # up to 4, 8 and 16 rows; one, two and many groups of a wave, with and without a rest
+               (1, 40, 7200), (4, 100, 2560), (6, 200, 4608), (7, 4200, 1536), (8, 12290, 4128), (9, 60, 2048),
+               (11, 4200, 5152), (13, 96, 12288), (16, 8300, 4096), (16, 12300, 4128), (16, 12300, 2560),
+               (17, 33, 160), (31, 129, 2048), (33, 200, 608), (48, 77, 1024), (64, 512, 96),
                (65, 1, 32), (65, 130, 96), (100, 257, 544), (128, 128, 1024), (129, 385, 480), (256, 512, 256),
                (257, 300, 768), (300, 515, 2080), (512, 96, 12288), (700, 1030, 160)]
 
