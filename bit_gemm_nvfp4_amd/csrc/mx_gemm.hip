@@ -20,6 +20,7 @@
 
 #include "internal.h"
 #include "mx.h"
+#include "mx_bounds.h"
 
 namespace nvfp4 {
 
@@ -118,17 +119,19 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A,
             product(w[0], a);
         }
     } else {
-        // Codes of full groups come through a buffer of the workgroup's rows; those of groups past the last full
-        // one from an empty one.
+        // Codes of full groups come through a buffer of the workgroup's rows (a row past N repeats the last one);
+        // those of groups past the last full one from an empty one.
         const int row_bytes = K / 2, rows = (int)min((int64_t)16 * RT, N - n0);
-        const uint32_t voff = (uint32_t)(r * row_bytes + lg * 16);
+        uint32_t voff[RT];
+#pragma unroll
+        for (int t = 0; t < RT; t++) voff[t] = (uint32_t)(min(16 * t + r, rows - 1) * row_bytes + lg * 16);
         auto load_codes = [&](MxGroup (&w)[RT], int g, int i) {
-            const __amdgpu_buffer_rsrc_t rw =
-                uniform_rsrc(wcodes + n0 * row_bytes, g < full ? (uint32_t)(rows * row_bytes) : 0u);
+            const uint32_t bytes = g < full ? (uint32_t)(rows * row_bytes) : 0u;
+            const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(wcodes + n0 * row_bytes, bytes);
+            const uint32_t soff = bounds::part_soff((uint32_t)g * (kGroup / 2), bytes);
 #pragma unroll
             for (int t = 0; t < RT; t++)
-                w[t].c[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(voff + i * 64),
-                                                                  g * (kGroup / 2) + t * 16 * row_bytes, 0);
+                w[t].c[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(voff[t] + i * 64), (int)soff, 0);
         };
         auto load_scales = [&](MxGroup (&w)[RT], int g) {
 #pragma unroll
@@ -428,11 +431,9 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     const int h = lane >> 5;
     const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
     const int K = (int)p.K, kb = K / kMxBlock;
-    const int arb = (int)p.a_row_bytes, wrb = K / 2;  // below 2^23
+    const int arb = (int)p.a_row_bytes, wrb = K / 2;  // at most 2^23
     const int alen = (int)p.a_row_len, wlen = wrb;    // bytes of a row
     const int mrows = min(T::BM, (int)p.M - tm * T::BM), nrows = min(T::BN, (int)p.N - tn * T::BN);
-    const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(p.a + m0 * arb, (uint32_t)((mrows - 1) * arb + alen));
-    const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(p.wcodes + n0 * wrb, (uint32_t)(nrows * wrb));
 
     const int windows = (K + kGroup - 1) / kGroup;
     const int w0 = (int)blockIdx.y * p.slice_windows, w1 = min(w0 + p.slice_windows, windows);
@@ -440,23 +441,31 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     const int nsteps = min((w1 - w0) * T::WINDOW_STEPS, (K + T::BK - 1) / T::BK - step0);
 
     // Direct-to-LDS loads: unit u = wave + NW i fills 1 KiB of a stage (8 rows of 128 bytes, or 32 of 32).
-    // The rows of a wave's units differ by multiples of 32, so the lane part of the offset and the
-    // swizzle are the same for all of them and the rest is a scalar offset.  Rows past M or N lie past
-    // the buffer's range and load zeros; so do pieces past the end of a row (kOffsetPastRange).
+    // The units i of all waves have a buffer of their own over the rows that they cover, so the lane
+    // part of the offset and the swizzle are the same for all i and the scalar offset is the step's column.  Rows past
+    // M or N lie past the buffer's range and load zeros; so do pieces past the end of a row (mx_bounds.h).
     constexpr int A_PER = T::A_UNITS / T::NW, RPU = 64 / T::W_PIECES;
     const int ar = wave * 8 + lane / 8, wr = wave * RPU + lane / T::W_PIECES;
     const int apb = swizzle<8>(ar, lane % 8) * 16, wpb = swizzle<T::W_PIECES>(wr, lane % T::W_PIECES) * 16;
-    const uint32_t avo = (uint32_t)(ar * arb + apb), wvo = (uint32_t)(wr * wrb + wpb);
+    __amdgpu_buffer_rsrc_t rsrc[T::UPW];
+    uint32_t bytes[T::UPW];
+#pragma unroll
+    for (int i = 0; i < T::UPW; i++) {
+        const bool is_a = i < A_PER;
+        const bounds::Part part = is_a ? bounds::rows_part(i * (T::NW * 8), T::NW * 8, mrows, arb, alen)
+                                       : bounds::rows_part((i - A_PER) * (T::NW * RPU), T::NW * RPU, nrows, wrb, wlen);
+        bytes[i] = (uint32_t)__builtin_amdgcn_readfirstlane(part.bytes);
+        rsrc[i] = uniform_rsrc((is_a ? p.a + m0 * arb : p.wcodes + n0 * wrb) + part.base, part.bytes);
+    }
     auto load_stage = [&](int s) {  // step s of the slice
         uint8_t *dst = lds + (s % T::NST) * T::STAGE + wave * 1024;
         const int ao = (step0 + s) * T::A_ROWB, wo = (step0 + s) * T::W_ROWB;
-        const uint32_t av = ao + apb < alen ? avo : kOffsetPastRange;
-        const uint32_t wv = wo + wpb < wlen ? wvo : kOffsetPastRange;
+        const uint32_t av = bounds::lane_off((uint32_t)(ar * arb), ao, apb, alen);
+        const uint32_t wv = bounds::lane_off((uint32_t)(wr * wrb), wo, wpb, wlen);
 #pragma unroll
-        for (int i = 0; i < T::UPW; i++) {
-            if (i < A_PER) load_to_lds16(ra, dst + i * (T::NW * 1024), av, ao + i * (T::NW * 8) * arb);
-            else load_to_lds16(rw, dst + i * (T::NW * 1024), wv, wo + (i - A_PER) * (T::NW * RPU) * wrb);
-        }
+        for (int i = 0; i < T::UPW; i++)
+            load_to_lds16(rsrc[i], dst + i * (T::NW * 1024), i < A_PER ? av : wv,
+                          bounds::part_soff(i < A_PER ? ao : wo, bytes[i]));
     };
     // scale rows [A rows (MXFP4 A), W rows]: thread tid serves rows tid, tid + NT, ...
     const uint8_t *srow[T::SC_PER];
