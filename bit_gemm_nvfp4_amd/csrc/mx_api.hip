@@ -23,8 +23,8 @@ int elem_bytes(nvfp4_dtype dt) {
     }
 }
 
-// Sizes the kernels index with: rows and columns below 2^31, K small enough for a tile's rows to stay
-// within the 2 GiB range of a buffer resource.
+// Sizes the kernels index with: rows and columns below 2^31, rows short enough for those that share a buffer to stay
+// within 2^29 bytes (64 rows of A, 256 rows of W), the limits themselves included.
 constexpr int64_t kMaxDim = 0x7FFFFFFF, kMaxK = (int64_t)1 << 22, kMaxTileLd = (int64_t)1 << 22;
 
 nvfp4_status check_mx(const mxfp4_tensor *t) {
