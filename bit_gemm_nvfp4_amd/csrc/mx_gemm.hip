@@ -21,13 +21,14 @@
 #include "internal.h"
 #include "mx.h"
 #include "mx_bounds.h"
+#include "mx_plan.h"
 
 namespace nvfp4 {
 
 namespace {
 
 constexpr int kSkinnyMaxM = 16;
-constexpr int kMaxSplits = 8;  // K slices of a tiled product
+static_assert(kPlanWindow == kGroup, "K slices are whole windows of scale bytes");
 
 template <class OT>
 __device__ __forceinline__ void store_out(OT *p, float v) {
@@ -727,67 +728,6 @@ __global__ __launch_bounds__(256) void k_mx_zero(OT *C, int64_t M, int64_t N, in
 // -------------------------------------------------------------------------------------------------
 // launches
 // -------------------------------------------------------------------------------------------------
-struct MxPlan {
-    int cfg;            // index into the tile shapes
-    int splits;         // K slices
-    int slice_windows;  // windows of 512 columns per slice
-};
-
-// Tile shapes and what they cost: microseconds per tile (start, first loads, stores) and per window of 512
-// columns, with one workgroup per CU and with `per_cu` of them.  Fitted to timings of every shape with 1, 2
-// and 4 K slices on an MI355X; of those, in microseconds (tile: time; the shape picked is marked):
-//   W4A4   512 x 12288 x 4096   256x256: 33.1   128x256: 23.9 *  128x128: 30.3   64x128: 29.8   64x64: 36.6
-//   W4A4   512 x 4096 x 12288   128x256: 53.4   128x128: 34.7 (two slices: 31.4)   64x128: 27.7 *  64x64: 32.4
-//   W4A4   4096 x 4096 x 4096   256x256: 40.1 * 128x256: 45.2    128x128: 54.1
-//   W4A4   1024 x 4096 x 4096   128x256: 20.2   128x128: 15.6 *  64x128: 18.6   64x64: 22.9
-//   W4A4   256 x 4096 x 4096    128x256: 18.7   128x128: 12.8    64x128: 10.0   64x64: 8.7 *
-//   W4A16  512 x 12288 x 4096   256x256: 81.4   128x256: 50.1 *  128x128: 55.5   64x128: 60.3
-//   W4A16  512 x 4096 x 12288   128x256: 128.4, in four slices 59.1 *  128x128 in two: 64.2
-//   W4A16  128 x 4096 x 4096    128x128: 35.6   64x128: 24.6, in four slices 16.9 *  32x128 in two: 17.3
-//   W4A16  17 x 12288 x 4096    64x128: 24.7, in four slices 16.6   32x128: 21.0, in four slices 14.8 *
-//   W4A16  4096 x 12288 x 4096  256x256: 313 *  128x256: 359     128x128: 361
-struct TileCost {
-    int bm, bn, per_cu;
-    double start, window, window_full;
-};
-constexpr int kTileShapes = 5;
-constexpr TileCost kTileCost[2][kTileShapes] = {
-    {{256, 256, 1, 3.0, 12.6, 12.6},
-     {128, 256, 1, 5.0, 6.4, 6.4},
-     {128, 128, 2, 4.0, 4.0, 7.0},
-     {64, 128, 2, 3.0, 2.8, 4.5},
-     {32, 128, 2, 3.0, 2.1, 3.0}},
-    {{256, 256, 1, 7.8, 3.84, 3.84},
-     {128, 256, 1, 5.0, 2.4, 2.4},
-     {128, 128, 1, 2.5, 1.5, 1.5},
-     {64, 64, 2, 2.4, 0.82, 1.2},
-     {64, 128, 2, 2.5, 1.05, 1.8}},
-};
-constexpr double kReduceStart = 4.0, kReduceBytesPerUs = 3.0e6;  // the pass that adds the slices
-
-MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
-    const int64_t windows = (K + kGroup - 1) / kGroup;
-    MxPlan best{0, 1, (int)windows};
-    double cost = 1e30;
-    for (int cfg = 0; cfg < kTileShapes; cfg++) {
-        const TileCost &t = kTileCost[a_mx ? 1 : 0][cfg];
-        const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
-        for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplits, windows); s++) {
-            const int64_t per = (windows + s - 1) / s;
-            if ((windows + per - 1) / per != s) continue;  // a slice would be empty
-            const int64_t all = tiles * s, slots = (int64_t)num_cus * t.per_cu;
-            double us = all <= num_cus ? t.start + per * t.window
-                                       : (double)((all + slots - 1) / slots) * (t.start + per * t.window_full);
-            if (s > 1) us += kReduceStart + (double)M * N * 4 * (s + 1) / kReduceBytesPerUs;
-            if (us < cost) {
-                cost = us;
-                best = MxPlan{cfg, (int)s, (int)per};
-            }
-        }
-    }
-    return best;
-}
-
 template <class T, class OT>
 void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) {
     p.tiles_m = (int)((p.M + T::BM - 1) / T::BM);
@@ -829,11 +769,7 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
     p.ascales = a_mx ? a_q->scales : nullptr;
     p.a_row_bytes = a_mx ? p.K / 2 : lda * 2;
     p.a_row_len = a_mx ? p.K / 2 : p.K * 2;
-    MxPlan plan = plan_mx(M, p.N, p.K, a_mx, num_cus);
-    if (plan.splits > 1 && (!workspace || workspace_bytes < (size_t)plan.splits * M * p.N * 4)) {
-        plan.splits = 1;
-        plan.slice_windows = (int)((p.K + kGroup - 1) / kGroup);
-    }
+    const MxPlan plan = plan_mx_within(M, p.N, p.K, a_mx, num_cus, workspace ? workspace_bytes : 0);
     p.slice_windows = plan.slice_windows;
     if (a_mx) {
         switch (plan.cfg) {
@@ -911,8 +847,7 @@ hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t
 
 size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
     if (M <= kSkinnyMaxM || N <= 0 || K <= 0) return 0;
-    const MxPlan plan = plan_mx(M, N, K, a_mx, num_cus);
-    return plan.splits > 1 ? (size_t)plan.splits * M * N * 4 : 0;
+    return plan_ws_bytes(plan_mx(M, N, K, a_mx, num_cus), M, N);
 }
 
 hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
