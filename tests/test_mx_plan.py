@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+import mx_shapes
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "bit_gemm_nvfp4_amd", "csrc")
 CUS = 256
@@ -77,6 +79,17 @@ def test_without_its_workspace_a_product_takes_the_shape_that_is_cheapest_in_one
             assert ask.plan(m, n, k, mx, have) == one
         seen.add((cfg != one[0], splits > 1))
     assert (True, True) in seen  # the shapes of the two forms do differ somewhere
+
+
+def test_the_products_of_the_gpu_tests_reach_every_shape(ask):
+    reached = set()
+    for (m, n, k), act, tile, splits in mx_shapes.PRODUCTS:
+        mx = int(act == "mx")
+        cfg, s, _ = ask.plan(m, n, k, mx)
+        assert (ask.tile(mx, cfg), s) == (tile, splits), (m, n, k, act, ask.tile(mx, cfg), s)
+        assert m % tile[0] and n % tile[1] and k % (256 if mx else 64) and n > tile[1] and n % 8 == 0
+        reached.add((mx, cfg, s > 1))
+    assert reached == {(mx, cfg, split) for mx in (0, 1) for cfg in range(ask.shapes) for split in (False, True)}
 
 
 def test_the_kernels_are_the_shapes_of_the_table(ask):

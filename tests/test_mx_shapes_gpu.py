@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+import mx_ref
+import mx_shapes
 from gpu_util import DEV
 
 pytestmark = pytest.mark.gpu
@@ -11,6 +13,51 @@ pytestmark = pytest.mark.gpu
 def nv():
     import bit_gemm_nvfp4_amd as m
     return m
+
+
+def _random(nv, g, rows, cols):
+    """Random codes and scale bytes, every block with its own, and the values they stand for in float64."""
+    codes = torch.randint(0, 256, (rows, cols // 2), generator=g, dtype=torch.uint8, device=DEV)
+    scales = torch.randint(117, 130, (rows, cols // 32), generator=g, dtype=torch.uint8, device=DEV)
+    table = torch.tensor([*mx_ref.E2M1, *-mx_ref.E2M1], dtype=torch.float64, device=DEV)
+    v = torch.stack((table[(codes & 15).int()], table[(codes >> 4).int()]), dim=2).view(rows, cols // 32, 32)
+    v *= torch.exp2(scales.double() - 127).unsqueeze(2)
+    return nv.MXFP4Tensor(codes, scales), v.view(rows, cols)
+
+
+@pytest.mark.parametrize("case", mx_shapes.PRODUCTS, ids=lambda c: "x".join(map(str, c[0])) + "-" + c[1])
+def test_every_tile_shape(nv, case):
+    (m, n, k), act, _, splits = case
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m * n + k)
+    w, wd = _random(nv, g, n, k)
+    if act == "mx":
+        a, ad = _random(nv, g, m, k)
+    else:
+        a = (torch.randn((m, k), generator=g, device=DEV) *
+             torch.exp2(torch.randint(-6, 4, (m, k), generator=g, device=DEV).float())).to(torch.bfloat16)
+        ad = a.double()
+    ref, mag = ad @ wd.t(), ad.abs() @ wd.abs().t()
+    bound = mx_ref.fp32_sum_bound(1, k) * mag
+
+    def check(c):
+        half = 2.0 ** -8 if c.dtype == torch.bfloat16 else 2.0 ** -24
+        over = (c.double() - ref).abs() - bound - half * ref.abs() - 1e-38
+        assert float(over.max()) <= 0, (int(over.argmax()) // n, int(over.argmax()) % n)
+        return c
+    ws = nv.mx_gemm_workspace(a, w)
+    assert (ws is not None) == (splits > 1)
+    f = check(nv.mx_gemm(a, w, workspace=ws))
+    b = check(nv.mx_gemm(a, w, dtype=torch.bfloat16, workspace=ws))
+    assert torch.equal(f.to(torch.bfloat16), b)
+    # rows of C that allow no wide store, what lies around them left as it was
+    buf = torch.full((m + 1, n + 3), 7.0, device=DEV)
+    nv.mx_gemm(a, w, out=buf[:m, 1:n + 1], workspace=ws)
+    assert torch.equal(buf[:m, 1:n + 1], f)
+    buf[:m, 1:n + 1] = 7
+    assert bool((buf == 7).all())
+    if splits > 1:  # in one piece, the shape that is cheapest then
+        check(nv.mx_gemm(a, w, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)))
 
 
 def test_longest_rows_in_the_largest_tile(nv):
