@@ -26,6 +26,8 @@ int elem_bytes(nvfp4_dtype dt) {
 // Sizes the kernels index with: rows and columns below 2^31, rows short enough for those that share a buffer to stay
 // within 2^29 bytes (64 rows of A, 256 rows of W), the limits themselves included.
 constexpr int64_t kMaxDim = 0x7FFFFFFF, kMaxK = (int64_t)1 << 22, kMaxTileLd = (int64_t)1 << 22;
+// Rows whose tiles fit one launch in the largest tile shape.
+constexpr int64_t kMaxTileDim = ((int64_t)1 << 31) - (1 << 11);
 
 nvfp4_status check_mx(const mxfp4_tensor *t) {
     if (!t) return NVFP4_ERR_NULL;
@@ -99,6 +101,7 @@ nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
     const int64_t N = w->rows, K = w->cols;
     if (c_dtype != NVFP4_F32 && c_dtype != NVFP4_BF16) return NVFP4_ERR_DTYPE;
     if (M < 0 || M > kMaxDim || K > kMaxK) return NVFP4_ERR_SHAPE;
+    if (M > 16 && (M > kMaxTileDim || N > kMaxTileDim)) return NVFP4_ERR_SHAPE;
     // rows of A without elements need no pointer
     if (a_bf16 && a_q) return NVFP4_ERR_ARG;
     if (!a_bf16 && !a_q && M > 0 && K > 0) return NVFP4_ERR_ARG;

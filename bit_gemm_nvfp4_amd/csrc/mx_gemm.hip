@@ -732,8 +732,7 @@ template <class T, class OT>
 void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) {
     p.tiles_m = (int)((p.M + T::BM - 1) / T::BM);
     p.tiles_n = (int)((p.N + T::BN - 1) / T::BN);
-    const int per = (p.tiles_m * p.tiles_n + 7) / 8;
-    const dim3 grid(per * 8, splits);
+    const dim3 grid((unsigned)tile_grid((int64_t)p.tiles_m * p.tiles_n), splits);
     if (splits == 1) {
         p.vec_c = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc * sizeof(OT) % 16 == 0;
         hipLaunchKernelGGL((k_mx_tile<T, OT, false>), grid, dim3(T::NT), 0, stream, p);
@@ -754,8 +753,8 @@ void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) 
 }
 
 template <class OT>
-void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
-                  int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, hipStream_t stream) {
+hipError_t launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
+                        int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, hipStream_t stream) {
     MxTileArgs p{};
     p.M = M;
     p.N = w->rows;
@@ -770,6 +769,7 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
     p.a_row_bytes = a_mx ? p.K / 2 : lda * 2;
     p.a_row_len = a_mx ? p.K / 2 : p.K * 2;
     const MxPlan plan = plan_mx_within(M, p.N, p.K, a_mx, num_cus, workspace ? workspace_bytes : 0);
+    if (plan.cfg < 0) return hipErrorInvalidConfiguration;
     p.slice_windows = plan.slice_windows;
     if (a_mx) {
         switch (plan.cfg) {
@@ -788,6 +788,7 @@ void launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_
         default: launch_tile_t<MxTile<32, 128, 1, 4, false, 4>, OT>(p, plan.splits, workspace, stream); break;
         }
     }
+    return hipGetLastError();
 }
 
 template <int RT, int MR, class OT>
@@ -838,7 +839,7 @@ hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t
         else if (M <= 8) launch_skinny<8>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
         else launch_skinny<16>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
     } else {
-        launch_tiled(a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
+        return launch_tiled(a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     }
     return hipGetLastError();
 }

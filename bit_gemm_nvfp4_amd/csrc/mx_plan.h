@@ -10,7 +10,7 @@ constexpr int kMaxSplits = 8;     // K slices of a tiled product
 constexpr int kPlanWindow = 512;  // columns that a slice is a multiple of
 
 struct MxPlan {
-    int cfg;            // index into the tile shapes
+    int cfg;            // index into the tile shapes, -1 when the tiles of none fit one launch
     int splits;         // K slices
     int slice_windows;  // windows of 512 columns per slice
 };
@@ -29,32 +29,37 @@ struct MxPlan {
 //   W4A16  17 x 12288 x 4096    64x128: 24.7, in four slices 16.6   32x128: 21.0, in four slices 14.8 *
 //   W4A16  4096 x 12288 x 4096  256x256: 313 *  128x256: 359     128x128: 361
 struct TileCost {
-    int bm, bn, per_cu;
+    int bm, bn, waves, per_cu;
     double start, window, window_full;
 };
 constexpr int kTileShapes = 5;
 constexpr TileCost kTileCost[2][kTileShapes] = {
-    {{256, 256, 1, 3.0, 12.6, 12.6},
-     {128, 256, 1, 5.0, 6.4, 6.4},
-     {128, 128, 2, 4.0, 4.0, 7.0},
-     {64, 128, 2, 3.0, 2.8, 4.5},
-     {32, 128, 2, 3.0, 2.1, 3.0}},
-    {{256, 256, 1, 7.8, 3.84, 3.84},
-     {128, 256, 1, 5.0, 2.4, 2.4},
-     {128, 128, 1, 2.5, 1.5, 1.5},
-     {64, 64, 2, 2.4, 0.82, 1.2},
-     {64, 128, 2, 2.5, 1.05, 1.8}},
+    {{256, 256, 8, 1, 3.0, 12.6, 12.6},
+     {128, 256, 8, 1, 5.0, 6.4, 6.4},
+     {128, 128, 4, 2, 4.0, 4.0, 7.0},
+     {64, 128, 4, 2, 3.0, 2.8, 4.5},
+     {32, 128, 4, 2, 3.0, 2.1, 3.0}},
+    {{256, 256, 8, 1, 7.8, 3.84, 3.84},
+     {128, 256, 8, 1, 5.0, 2.4, 2.4},
+     {128, 128, 8, 1, 2.5, 1.5, 1.5},
+     {64, 64, 4, 2, 2.4, 0.82, 1.2},
+     {64, 128, 4, 2, 2.5, 1.05, 1.8}},
 };
+constexpr uint64_t kMaxGridThreads = 0xFFFFFFFFull;  // of one launch, in x
 constexpr double kReduceStart = 4.0, kReduceBytesPerUs = 3.0e6;  // the pass that adds the slices
+
+// Workgroups of a product's tiles: whole rounds over the eight XCDs.
+inline int64_t tile_grid(int64_t tiles) { return (tiles + 7) / 8 * 8; }
 
 // The cheapest of the shapes and of up to `max_splits` K slices.
 inline MxPlan plan_mx(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus, int max_splits = kMaxSplits) {
     const int64_t windows = (K + kPlanWindow - 1) / kPlanWindow;
-    MxPlan best{0, 1, (int)windows};
+    MxPlan best{-1, 1, (int)windows};
     double cost = 1e30;
     for (int cfg = 0; cfg < kTileShapes; cfg++) {
         const TileCost &t = kTileCost[a_mx ? 1 : 0][cfg];
         const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+        if ((uint64_t)tile_grid(tiles) * 64 * t.waves > kMaxGridThreads) continue;
         for (int64_t s = 1; s <= max_splits && s <= windows; s++) {
             const int64_t per = (windows + s - 1) / s;
             if ((windows + per - 1) / per != s) continue;  // a slice would be empty

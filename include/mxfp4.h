@@ -79,7 +79,7 @@ nvfp4_status mxfp4_dequantize(const mxfp4_tensor *in, void *out, nvfp4_dtype out
  * workspace (16-byte aligned, or NULL): with mxfp4_workspace_size(MXFP4_OP_GEMM_BF16 or _MX, M, N, K) bytes a
  * long K is split over workgroups where there are few output tiles (fp32 partial sums, added in slice
  * order); with less, or NULL, the product runs unsplit, in the tile shape that is cheapest then.  K <= 2^22,
- * and for M > 16 lda <= 2^22 (NVFP4_ERR_SHAPE).  K == 0 gives C = 0.
+ * and for M > 16 lda <= 2^22, M and N at most 2^31 - 2^11 (NVFP4_ERR_SHAPE).  K == 0 gives C = 0.
  */
 nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                         void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,

@@ -18,6 +18,7 @@ using namespace nvfp4;
 extern "C" int shapes() { return kTileShapes; }
 extern "C" int max_splits() { return kMaxSplits; }
 extern "C" void shape(int mx, int cfg, int *bm, int *bn) { *bm = kTileCost[mx][cfg].bm; *bn = kTileCost[mx][cfg].bn; }
+extern "C" int waves(int mx, int cfg) { return kTileCost[mx][cfg].waves; }
 extern "C" void plan(int64_t m, int64_t n, int64_t k, int mx, int cus, uint64_t have, int *out) {
     const MxPlan p = plan_mx_within(m, n, k, mx, cus, have);
     out[0] = p.cfg; out[1] = p.splits; out[2] = p.slice_windows;
@@ -49,6 +50,10 @@ def ask(tmp_path_factory):
             bm, bn = ctypes.c_int(), ctypes.c_int()
             lib.shape(mx, cfg, ctypes.byref(bm), ctypes.byref(bn))
             return bm.value, bn.value
+
+        @staticmethod
+        def waves(mx, cfg):
+            return lib.waves(mx, cfg)
 
         @staticmethod
         def plan(m, n, k, mx, have=ALL):
@@ -95,5 +100,28 @@ def test_the_products_of_the_gpu_tests_reach_every_shape(ask):
 def test_the_kernels_are_the_shapes_of_the_table(ask):
     text = open(os.path.join(CSRC, "mx_gemm.hip")).read()
     for mx, word in ((0, "false"), (1, "true")):
-        found = re.findall(r"launch_tile_t<MxTile<(\d+), (\d+), \d+, \d+, %s, \d+>" % word, text)
-        assert [(int(a), int(b)) for a, b in found] == [ask.tile(mx, c) for c in range(ask.shapes)]
+        found = re.findall(r"launch_tile_t<MxTile<(\d+), (\d+), (\d+), (\d+), %s, \d+>" % word, text)
+        assert [(int(a), int(b), int(c) * int(d)) for a, b, c, d in found] == \
+            [(*ask.tile(mx, c), ask.waves(mx, c)) for c in range(ask.shapes)]
+
+
+@pytest.mark.parametrize("mx", [0, 1])
+def test_one_launch_holds_the_tiles(ask, mx):
+    most = (1 << 31) - (1 << 11)
+    assert ask.plan(1 << 31, 1 << 31, 32, mx)[0] < 0
+    for m, n in ((1 << 28, 3), (1 << 30, 1), ((1 << 30) + 100, 1), (most, 1), (17, most), (1 << 20, 1 << 11)):
+        cfg, _, _ = ask.plan(m, n, 32, mx)
+        bm, bn = ask.tile(mx, cfg)
+        tiles = -(-m // bm) * -(-n // bn)
+        assert -(-tiles // 8) * 8 * 64 * ask.waves(mx, cfg) < 1 << 32, (m, n)
+
+
+def test_products_of_more_tiles_than_a_launch_holds_are_refused():
+    import bit_gemm_nvfp4_amd as nv
+    from bit_gemm_nvfp4_amd.mx import CMXTensor
+    fake, most = 0x10000, (1 << 31) - (1 << 11)  # 16-byte aligned, never dereferenced
+
+    def call(m, n):
+        a, w = CMXTensor(fake, fake, m, 32), CMXTensor(fake, fake, n, 32)
+        return nv.lib.mxfp4_gemm(None, ctypes.byref(a), m, 0, ctypes.byref(w), ctypes.c_void_p(fake), 0, n, None, 1 << 40, None)
+    assert call(most + 1, 1) == 2 and call(17, most + 1) == 2

@@ -77,3 +77,15 @@ def test_longest_rows_in_the_largest_tile(nv):
     want[:, 5] = x + 2 * y
     want[:, n - 1] = 2 * x + y
     assert torch.equal(c, want)
+
+
+def test_more_rows_than_small_tiles_fit_in_a_launch(nv):
+    m = (1 << 30) + 100  # in tiles of 64 rows, more threads than one launch can have
+    a = nv.MXFP4Tensor(torch.zeros((m, 16), dtype=torch.uint8, device=DEV),
+                       torch.full((m, 1), 127, dtype=torch.uint8, device=DEV))
+    w = nv.MXFP4Tensor(torch.full((1, 16), 0x22, dtype=torch.uint8, device=DEV),
+                       torch.full((1, 1), 127, dtype=torch.uint8, device=DEV))
+    rows = torch.tensor([0, 12345, 1 << 29, m - 101, m - 1], device=DEV)
+    a.codes[rows] = 0x44
+    c = nv.mx_gemm(a, w, dtype=torch.bfloat16)
+    assert bool((c[rows] == 64).all()) and int((c != 0).sum()) == len(rows)
