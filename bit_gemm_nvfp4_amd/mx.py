@@ -69,8 +69,9 @@ class MXFP4Tensor:
 
 
 # The binding's own time is most of a small call's, so it takes the raw current stream of the device and
-# switches devices only when the tensors are not on the current one.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# switches devices only when the tensors are not on the current one.  Like the library, what torch has only in
+# builds for GPUs is looked up at the first call.
+_raw_stream = None
 _current_device = torch.cuda.current_device
 
 
@@ -78,9 +79,9 @@ _functions: dict = {}
 
 
 def _function(name: str):
-    fn = _functions.get(name)
-    if fn is None:
-        fn = _functions[name] = getattr(load_library(), name)
+    global _raw_stream
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    fn = _functions[name] = getattr(load_library(), name)
     return fn
 
 
