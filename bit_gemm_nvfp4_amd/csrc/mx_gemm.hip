@@ -149,14 +149,15 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A,
                               mine + (b * MR + m) * kStageRow, lane * 16, 0);
             }
             // what arrived() counts as behind these loads stays behind them
-            asm volatile("" ::: "memory");
+            asm volatile("; rows staged" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
         };
-        // all but the last n loads have arrived, those into LDS among them
+        // All but the last n loads have arrived, those into LDS among them.  That holds only if the compiled code has
+        // n loads between the two marks on every way there; tests/test_mx_waits.py counts them.
         auto arrived = [](auto n) {
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(waitcnt_imm(n, 15));
-            asm volatile("" ::: "memory");
+            asm volatile("; rows arrived, %0 loads behind" ::"n"(decltype(n)::value) : "memory");
             __builtin_amdgcn_sched_barrier(0);
         };
         auto product = [&](const MxGroup (&w)[RT], int b, int i) {
