@@ -360,10 +360,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
                 }
                 const int t = sh_tok[q + j];
                 const float h = silu(gs) * us * sh_p[t];
-                const __bf16 hi = (__bf16)h;
+                // A value that rounds beyond bf16's range is cut off instead, its rest goes into the low plane; an
+                // infinity or NaN has no rest.
+                const bool finite = (f2u(h) & 0x7F800000u) != 0x7F800000u;
+                __bf16 hi = (__bf16)h;
+                if (finite && (f2u((float)hi) & 0x7F800000u) == 0x7F800000u) hi = (__bf16)u2f(f2u(h) & 0xFFFF0000u);
                 __bf16 *dst = a.h + (int64_t)(t * a.k + sh_rank[t]) * 2 * a.I + (tile0 + c0) * 16 + ir;
                 dst[0] = hi;
-                dst[a.I] = (__bf16)(h - (float)hi);
+                dst[a.I] = finite ? (__bf16)(h - (float)hi) : (__bf16)0.0f;
             }
         }
     }
