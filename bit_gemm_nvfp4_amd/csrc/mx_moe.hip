@@ -17,7 +17,7 @@
 // expert by counting, and one further workgroup per token writes that token's choices and softmax sum.
 //   k_moe_up:   workgroup (slot, a run of 16-row tiles of the intermediate size): gate and up products of
 //               the slot's expert for the tokens that chose it, h = silu(g) u exp(logit - row max), stored
-//               as two bf16 planes (2^-17 of its value) per (token, choice).  With tokens * top_k <
+//               as three bf16 planes that add up to its fp32 value, per (token, choice).  With tokens * top_k <
 //               experts a slot is a (token, choice) pair, and a pair whose expert an earlier token chose
 //               is left empty; otherwise a slot is an expert.  The first run of a slot lists its tokens.
 //   k_moe_down: workgroup (16 rows of Wd): (slot, 512-column group) items dealt to the waves.  h carries the
@@ -40,6 +40,7 @@ constexpr int kMaxT = MXFP4_MOE_MAX_TOKENS, kMaxE = MXFP4_MOE_MAX_EXPERTS;
 constexpr int kUpWaves = 8, kDownWaves = 8;
 // k_moe_down's tall form: row tiles per workgroup, and the average tokens per expert from which it is taken.
 constexpr int kTallTiles = 4, kTallTokens = 2, kTallRows = 16 * kTallTiles;
+constexpr int kPlanes = 3;  // bf16 values that carry the 24 bits of an fp32 one
 constexpr int kUpTiles = 4;  // tiles whose sums a wave keeps before the waves join them
 
 struct MoeDev {
@@ -56,7 +57,7 @@ struct MoeDev {
     float *den;          // [T] softmax sum; NaN for a row with NaN or +inf
     int32_t *slot_n;     // [slots] tokens of the slot | expert << 16
     uint16_t *slot_tok;  // [slots][T] token | choice << 8
-    __bf16 *h;           // [T * k][2][I]: the two planes of a (token, choice)
+    __bf16 *h;           // [T * k][kPlanes][I]: the planes of a (token, choice)
     float *parts;        // [workgroups of k_moe_down][T][64], with several tokens per expert
     uint32_t *arrived;   // [64-row blocks of H], zeroed by k_moe_up
     int row_blocks;
@@ -178,6 +179,10 @@ __device__ __forceinline__ void route_token(const MoeDev &a, int t, int lane) {
         if (a.weights) a.weights[t * a.k + lane] = id >= 0 ? p / den : 0.0f;
     }
 }
+
+// lane i takes lane (i - N) mod 16 of its row of 16
+template <int N>
+constexpr int kDppRowRor = 0x120 + N;
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
@@ -360,23 +365,24 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeDev a) {
                 }
                 const int t = sh_tok[q + j];
                 const float h = silu(gs) * us * sh_p[t];
-                // A value that rounds beyond bf16's range is cut off instead, its rest goes into the low plane; an
-                // infinity or NaN has no rest.
+                // Three planes of eight bits each, cut off, so that none rounds beyond bf16's range and their sum is
+                // h itself (to 2^-133 where its last bits lie below that); an infinity or NaN has no rest.
                 const bool finite = (f2u(h) & 0x7F800000u) != 0x7F800000u;
-                __bf16 hi = (__bf16)h;
-                if (finite && (f2u((float)hi) & 0x7F800000u) == 0x7F800000u) hi = (__bf16)u2f(f2u(h) & 0xFFFF0000u);
-                __bf16 *dst = a.h + (int64_t)(t * a.k + sh_rank[t]) * 2 * a.I + (tile0 + c0) * 16 + ir;
-                dst[0] = hi;
-                dst[a.I] = finite ? (__bf16)(h - (float)hi) : (__bf16)0.0f;
+                const float hi = u2f(f2u(h) & 0xFFFF0000u), rest = finite ? h - hi : 0.0f;
+                const float mid = u2f(f2u(rest) & 0xFFFF0000u);
+                __bf16 *dst = a.h + (int64_t)(t * a.k + sh_rank[t]) * kPlanes * a.I + (tile0 + c0) * 16 + ir;
+                dst[0] = (__bf16)(finite ? hi : h);
+                dst[a.I] = (__bf16)mid;
+                dst[2 * a.I] = (__bf16)(rest - mid);
             }
         }
     }
 }
 
-// Eight tokens at a time: columns 0-7 of the matrix instruction take the high planes of their h, columns 8-15
-// the low planes, and the two halves of the result are added.  A unit of work is eight tokens of a slot and a
-// 512-column group; units are dealt to the waves in turn.
-constexpr int kDownTokens = 8;
+// Five tokens at a time: columns 0-4 of the matrix instruction take the high planes of their h, columns 5-9 and 10-14
+// the others, and the three parts of the result are added (column 15 repeats a value that is not used).  A unit of work
+// is five tokens of a slot and a 512-column group; units are dealt to the waves in turn.
+constexpr int kDownTokens = 16 / kPlanes;
 constexpr int kDownEntries = kMaxE + kMaxT * MXFP4_MOE_MAX_TOP_K / kDownTokens;
 
 // RT: tiles of 16 rows that share a unit's activations.  RT = 1: one workgroup has all the units of its rows.
@@ -387,7 +393,7 @@ constexpr int kDownEntries = kMaxE + kMaxT * MXFP4_MOE_MAX_TOP_K / kDownTokens;
 template <class OT, int RT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
     extern __shared__ __align__(16) float sums[];  // [waves][T][16 RT]
-    __shared__ uint32_t sh_entry[kDownEntries];    // slot | eight-token pass << 9 | tokens of the slot << 16
+    __shared__ uint32_t sh_entry[kDownEntries];    // slot | pass over the tokens << 9 | tokens of the slot << 16
     __shared__ int sh_expert[kMaxE], sh_cnt[kDownWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     static_assert(kMaxE <= 64 * kDownWaves && kMaxE <= 512, "one thread per slot, nine bits");
@@ -415,7 +421,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
     __syncthreads();
     entries = __builtin_amdgcn_readfirstlane(entries);
 
-    const int r = lane & 15, lg = lane >> 4, plane = r / kDownTokens;
+    const int r = lane & 15, lg = lane >> 4, plane = min(r / kDownTokens, kPlanes - 1);
     const int kb = a.I / kMxBlock, full = a.I / kGroup, tail = kb - full * kGroupBlocks;
     const int groups = full + (tail > 0 ? 1 : 0), units = entries * groups;
     const int part = blockIdx.x % RT, n0 = blockIdx.x / RT * (16 * RT);
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
     };
     auto load_h = [&](int u, int tok) -> Bf16Group {
         const int g = u % groups;
-        const __bf16 *row = a.h + ((int64_t)((tok & 255) * a.k + (tok >> 8 & 255)) * 2 + plane) * a.I;
+        const __bf16 *row = a.h + ((int64_t)((tok & 255) * a.k + (tok >> 8 & 255)) * kPlanes + plane) * a.I;
         if (g < full) return load_bf16_group<false>(row, g, lg);
         return load_bf16_group<true>(row, g, lg, tail);
     };
@@ -452,11 +458,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
         group_product<RT>(w.t, h, lg, acc);
 #pragma unroll
         for (int t = 0; t < RT; t++) {
-            // columns c and c + 8 of a row of 16 lanes
+            // columns c, c + 5 and c + 10 of a row of 16 lanes, the smallest first
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float v = acc[t][i];
-                acc[t][i] = v + u2f(dpp_u32<kDppRowRor8>(f2u(v)));
+                acc[t][i] = v + (u2f(dpp_u32<kDppRowRor<16 - kDownTokens>>(f2u(v))) +
+                                 u2f(dpp_u32<kDppRowRor<16 - 2 * kDownTokens>>(f2u(v))));
             }
             if (r < kDownTokens && tok >> 16 == 0) {
                 f32x4 *dst = reinterpret_cast<f32x4 *>(&mine[(tok & 255) * (16 * RT) + t * 16 + lg * 4]);
@@ -592,7 +599,7 @@ size_t mx_moe_ws_bytes(int64_t pairs, int64_t hidden, int64_t inter) {
     if (pairs <= 0 || hidden <= 0 || inter <= 0) return 0;
     const size_t tokens = (size_t)std::min<int64_t>(pairs, kMaxT), blocks = (size_t)(hidden + kTallRows - 1) / kTallRows;
     return align256(kMaxT * 4) + align256(kMaxE * 4) + align256(kMaxE * tokens * 2) +
-           align256((size_t)pairs * inter * 4) + align256(blocks * 4) + blocks * kTallTiles * tokens * kTallRows * 4;
+           align256((size_t)pairs * inter * kPlanes * 2) + align256(blocks * 4) + blocks * kTallTiles * tokens * kTallRows * 4;
 }
 
 hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStream_t stream) {
@@ -623,7 +630,7 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     a.slot_tok = reinterpret_cast<uint16_t *>(ws);
     ws += align256((size_t)kMaxE * a.T * 2);
     a.h = reinterpret_cast<__bf16 *>(ws);
-    ws += align256((size_t)a.T * a.k * a.I * 4);
+    ws += align256((size_t)a.T * a.k * a.I * kPlanes * 2);
     const int blocks = (a.H + kTallRows - 1) / kTallRows;
     a.arrived = reinterpret_cast<uint32_t *>(ws);
     a.parts = reinterpret_cast<float *>(ws + align256((size_t)blocks * 4));

@@ -102,8 +102,8 @@ nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
  *   y       [tokens x H] fp32 or bf16 (y_dtype), row stride ld_y
  *   ids, weights  optional [tokens x top_k], dense: the chosen experts in descending order of logit and
  *           their p; -1 and 0 where a row has fewer
- * H and I are multiples of 32.  Sums are fp32; between the two products the activations are carried as
- * two bf16 planes (their value to 2^-17).  The result does not depend on the order of execution.
+ * H and I are multiples of 32.  Sums are fp32, and the activations between the two products keep the bits of
+ * fp32 (as three bf16 planes).  The result does not depend on the order of execution.
  * Errors: NVFP4_ERR_SHAPE for tokens > 64, experts > 512, top_k > 16, H or I above 2^22, or operands that
  * disagree; NVFP4_ERR_ARG for top_k < 1, top_k > experts or a bad renormalize; NVFP4_ERR_WORKSPACE for less than
  * mxfp4_workspace_size(MXFP4_OP_MOE, tokens * top_k, H, I) bytes (16-byte aligned).

@@ -1,5 +1,6 @@
 """The MXFP4 expert layer on the GPU: the range and precision of what it carries between its products, and the
 sizes that reach its forms."""
+import numpy as np
 import pytest
 import torch
 
@@ -54,3 +55,33 @@ def test_infinite_inner_values_go_out_as_in_fp32(nv, t, e, sign):
     inf = float("inf") * sign
     assert bool((y[:, 0] == inf).all()) and bool((y[:, 1] == -inf).all())
     assert bool(torch.isnan(y[:, 2:]).all())  # infinity times zero
+
+
+@pytest.mark.parametrize("t, e, i", [(1, 1, 32), (3, 8, 96), (11, 2, 544), (64, 5, 160), (64, 300, 32)])
+def test_inner_values_keep_the_bits_of_fp32(nv, t, e, i):
+    # gate g of 8 bits (silu(g) = g from g = 104 on) and up b + c 2^-8 of 16 bits: the inner value g (b + c 2^-8) has
+    # 24 bits, exact in fp32, and each output element is one of them
+    h = 64
+    rng = np.random.default_rng(t + i)
+    gu, dn = _zeros(nv, e * 2 * i, h), _zeros(nv, e * h, i)
+
+    def put(w, row, col, code):
+        w.codes[row, col // 2] |= code << (4 * (col % 2))
+    for r in range(i):
+        rows = torch.arange(e, device=DEV) * 2 * i + r
+        put(gu, rows, r % 16, 2)
+        put(gu, rows + i, 16 + r * 5 % 16, 2)
+        put(gu, rows + i, 32 + r * 3 % 16, 2)
+    pick = np.array([o * 7 % i for o in range(h)])
+    for o in range(h):
+        put(dn, torch.arange(e, device=DEV) * h + o, int(pick[o]), 2 + 8 * (o % 2))
+    xd = np.zeros((t, h))
+    xd[:, :32] = rng.integers(128, 256, (t, 32))
+    xd[:, 32:48] = rng.integers(128, 256, (t, 16)) / 256
+    x = torch.from_numpy(xd).to(torch.bfloat16).to(DEV)
+    logits = torch.from_numpy(rng.standard_normal((t, e)).astype(np.float32)).to(DEV)
+    r = np.arange(i)
+    inner = xd[:, r % 16] * (xd[:, 16 + r * 5 % 16] + xd[:, 32 + r * 3 % 16])
+    want = inner[:, pick] * np.where(np.arange(h) % 2, -1, 1)
+    y = nv.mx_moe(x, logits, gu, dn, 1, dtype=torch.float32)
+    assert np.array_equal(y.double().cpu().numpy(), want)
