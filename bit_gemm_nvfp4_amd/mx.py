@@ -100,10 +100,11 @@ def _call(name: str, device: torch.device, *args) -> None:
 
 
 def _opt(t: torch.Tensor | None, device: torch.device, name: str, dtype: torch.dtype | None = None):
-    """Address of an optional tensor argument on `device`."""
+    """Address of an optional tensor argument on `device`; of a single `dtype` when one is given."""
     if t is None:
         return None
-    assert t.device == device and (dtype is None or t.dtype is dtype), f"{name}: {t.dtype} on {t.device}"
+    assert t.device == device and (dtype is None or t.dtype is dtype and t.numel() == 1), \
+        f"{name}: {t.numel()} x {t.dtype} on {t.device}"
     return t.data_ptr()
 
 
