@@ -73,9 +73,11 @@ nvfp4_status mxfp4_dequantize(const mxfp4_tensor *in, void *out, nvfp4_dtype out
  *   - a_q, an MXFP4 tensor [M x K] (W4A4), a_bf16 NULL; or
  *   - a_bf16 [M x K] bf16 (row stride lda; W4A16), a_q NULL.
  * Exactly one of the two must be given (NVFP4_ERR_ARG otherwise); lda is ignored for W4A4.  Products
- * are summed in fp32 and rounded once to c_dtype (NVFP4_F32 or NVFP4_BF16); W4A16 expands W exactly to
- * bf16 on chip.  A row of A with a NaN or an infinity gives NaN or infinity in that row of C and
- * nothing elsewhere; a NaN block of W gives NaN in its column of C.
+ * are summed in fp32, subnormal numbers included, and rounded once to c_dtype (NVFP4_F32 or NVFP4_BF16).
+ * W4A16 expands W on chip to bf16, which is exact below 2^128; a value of W beyond that (possible with scale
+ * bytes 253 and 254 only) is an infinity there, as mxfp4_dequantize gives it.  A row of A with a NaN or an
+ * infinity gives NaN or infinity in that row of C and nothing elsewhere; a NaN block of W gives NaN in its
+ * column of C.
  * workspace (16-byte aligned, or NULL): with mxfp4_workspace_size(MXFP4_OP_GEMM_BF16 or _MX, M, N, K) bytes a
  * long K is split over workgroups where there are few output tiles (fp32 partial sums, added in slice
  * order); with less, or NULL, the product runs unsplit, in the tile shape that is cheapest then.  K <= 2^22,
@@ -102,7 +104,7 @@ nvfp4_status mxfp4_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
  *   y       [tokens x H] fp32 or bf16 (y_dtype), row stride ld_y
  *   ids, weights  optional [tokens x top_k], dense: the chosen experts in descending order of logit and
  *           their p; -1 and 0 where a row has fewer
- * H and I are multiples of 32.  Sums are fp32, and the activations between the two products keep the bits of
+ * H and I are multiples of 32.  Weights are expanded to bf16 as in W4A16.  Sums are fp32, and the activations between the two products keep the bits of
  * fp32 (as three bf16 planes).  The result does not depend on the order of execution.
  * Errors: NVFP4_ERR_SHAPE for tokens > 64, experts > 512, top_k > 16, H or I above 2^22, or operands that
  * disagree; NVFP4_ERR_ARG for top_k < 1, top_k > experts or a bad renormalize; NVFP4_ERR_WORKSPACE for less than

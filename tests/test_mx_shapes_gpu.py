@@ -89,3 +89,38 @@ def test_more_rows_than_small_tiles_fit_in_a_launch(nv):
     a.codes[rows] = 0x44
     c = nv.mx_gemm(a, w, dtype=torch.bfloat16)
     assert bool((c[rows] == 64).all()) and int((c != 0).sum()) == len(rows)
+
+
+@pytest.mark.parametrize("m", [1, 6, 16, 40, 66])
+@pytest.mark.parametrize("act", ["mx", "bf16"])
+def test_smallest_and_largest_scales(nv, act, m):
+    # one column of C per scale byte and pattern of codes; products and sums of a few of them, exact in fp32 down to its
+    # subnormal numbers
+    patterns = [[1], [2], [7], [1, 2, 7], [9, 10, 7], [3, 5, 11, 6]]
+    n = 255 * len(patterns)
+    codes = torch.zeros((n, 16), dtype=torch.uint8, device=DEV)
+    for p, pat in enumerate(patterns):
+        for j, c in enumerate(pat):
+            codes[p::len(patterns), j] = c  # elements 0, 2, 4, ...
+    scales = (torch.arange(n, device=DEV) // len(patterns)).to(torch.uint8).view(n, 1)
+    w = nv.MXFP4Tensor(codes, scales)
+    table = torch.tensor([*mx_ref.E2M1, *-mx_ref.E2M1], dtype=torch.float64, device=DEV)
+    terms = table[codes.int()] * torch.exp2(scales.double() - 127)  # [n, 16] elements 0, 2, ...
+    for e in (0, -20, 1, 60):
+        a = torch.zeros((m, 32), dtype=torch.bfloat16, device=DEV)
+        a[:, ::2] = 2.0 ** e
+        c = nv.mx_gemm(nv.mx_quantize(a) if act == "mx" else a, w)
+        if act == "bf16":  # W as bf16: values from 2^128 on are infinities
+            big = terms.abs() >= 2.0 ** 128
+            v = torch.where(big, torch.copysign(torch.full_like(terms, float("inf")), terms), terms)
+        else:
+            v = terms
+        want = (v * 2.0 ** e).sum(dim=1)
+        exact = (want.abs() / 2.0 ** -149 % 1 == 0) | ~torch.isfinite(want)  # a multiple of fp32's smallest step
+        # the sums of the finite terms stay in fp32's range (-2^127 * 2 beside an infinity would be a NaN)
+        inside = torch.where(v.isfinite(), v, torch.zeros_like(v)).abs().sum(dim=1) * 2.0 ** e < 2.0 ** 128
+        keep = exact & inside
+        got = c.double()
+        ok = (got == want.float().double()) | (torch.isnan(got) & torch.isnan(want))
+        assert bool(ok[:, keep].all()), (e, (~ok & keep).nonzero()[:4].tolist())
+        assert int(keep.sum()) > n // 2
