@@ -8,8 +8,10 @@
 // Bound by HBM: source bytes in, 17/32 byte out per element.  A lane takes 8 elements (16 bytes of a
 // 16-bit source; 16 elements of a one-byte one), the four (two) lanes of a block agree on its largest
 // magnitude by DPP moves, and codes leave as one dword (two) per lane, consecutive lanes to consecutive
-// addresses; four chunks per lane are loaded before the first is used.  4096 x 12288: fp32 42.0 us (5.4 TB/s), bf16
-// 24.1 us (5.3 TB/s); a device copy of 1 GiB moves 5.07 TB/s.  Expand to bf16: 20.9 us (6.1 TB/s).
+// addresses; four chunks per lane are loaded before the first is used.  12288 x 4096, calls in a row over inputs of 1 GB
+// in turn, which the Infinity Cache does not hold: fp32 41.4 us (5.5 TB/s), bf16 25.0 us (5.1 TB/s); expand to bf16
+// 23.2 us (5.5 TB/s), to fp32 44.6 us (5.1 TB/s).  The same input again and again: 33.6, 21.6, 20.8 and 37.4 us.  A
+// device copy of 1 GiB moves 5.07 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"

@@ -8,11 +8,13 @@
 //   operand layout (MxGroup), the waves of a workgroup split K and add their partial tiles in LDS in
 //   wave order.  MXFP4 activations take v_mfma_scale_f32_16x16x128; bf16 activations take
 //   v_mfma_f32_16x16x32_bf16 on W expanded exactly to bf16 (half an instruction per element), with A staged in
-//   LDS.  Calls in a row, W4A16: 1 x 12288 x 4096 7.5 us, 3.6 TB/s of W; 13 x 4096 x 12288 11.8 us, where each
-//   workgroup's reading of all of A through L2 (320 KB beside 105 KB of W) comes on top of the stream of W.
+//   LDS.  Calls in a row, W4A16, over weights of 0.8 GB in turn: 1 x 12288 x 4096 7.7 us, 3.5 TB/s of W; 13 x 4096 x
+//   12288 12.7 us, where each workgroup's reading of all of A through L2 (320 KB beside 105 KB of W) comes on top of
+//   the stream of W.  The same weights again and again, from the Infinity Cache: 6.5 and 10.0 us.  The 16-row bf16 form
+//   keeps 45 to 50 scalar values in lanes of vector registers; nothing goes to memory.
 // k_mx_tile (M > 16): BM x BN output tile per workgroup, operands through LDS by direct-to-LDS loads,
 //   v_mfma_scale_f32_32x32x64 for MXFP4 activations, v_mfma_f32_32x32x16_bf16 for bf16 ones.  4096 x 12288 x
-//   4096: W4A4 111 us, 3.7 PFLOP/s; W4A16 327 us, 1.26 PFLOP/s.
+//   4096: W4A4 111 us, 3.7 PFLOP/s; W4A16 321 us, 1.28 PFLOP/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -804,7 +806,7 @@ void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int
 
 // W row tiles per workgroup and its waves.  Every workgroup reads all of A through L2 (16 rows of bf16 are 3.8
 // times a tile of W), so tiles share it, as many as spread over the CUs in one round, up to three (four
-// spill).  Measured, us (K = 4096 unless said), with 1, 2 and 3 tiles, the pick marked:
+// spill).  Measured, us (K = 4096 unless said, weights of up to 0.6 GB in turn), with 1, 2 and 3 tiles, the pick marked:
 //   bf16  1 x 12288: 9.0, 10.0, 7.5 *;  16 x 12288: 13.9, 12.9, 9.6 *;  16 x 12288, K = 12288: 35.8, 32.9, 24.5 *
 //   bf16  16 x 6000: 8.9, 6.9 *, 8.2;  8 x 8192: 7.9, 6.9 *, 7.3
 //   bf16  16 x 4096: 5.4 *, 6.6, 8.0;  13 x 4096, K = 12288: 11.8 *, 15.9, 20.7

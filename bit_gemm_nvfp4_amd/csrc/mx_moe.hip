@@ -6,8 +6,11 @@
 // are expanded exactly to bf16 (half an instruction per element) and multiply up to 16 tokens at a time with
 // v_mfma_f32_16x16x32_bf16.  Each wave has the weights of its next groups in flight while it works on one.
 // Measured with 64 experts of 4096 x 1536, kernel times and rate of the weights' bytes:
-//   1 token, 8 experts each    up 15.2 us (3.5 TB/s), down 10.2 us (2.6 TB/s)
-//   33 tokens, 4 experts each  up 91 us (4.2 TB/s), down 64 us (3.0 TB/s)
+//   1 token, 8 experts each    up 15.5 us (3.5 TB/s), down 11.2 us (2.4 TB/s)
+//   33 tokens, 4 experts each  up 92 us (4.2 TB/s), down 66 us (2.9 TB/s)
+// with the same weights again and again: the 80 MB of the one token come from the Infinity Cache, the 565 MB of the 33
+// do not fit it.  The layer's calls for one token: 26.6 us, over nine sets of weights in turn 28.5 us.
+// Figures marked "two planes" below compare forms as they were before h had its third one.
 // A copy of 1 GiB moves 5.07 TB/s.  What is lost: about 4 us of each launch pass before its first weights arrive
 // and after the last (logits or slot lists, sums over the waves), and k_moe_down deals whole units to the waves
 // (6 rounds for 5.3 units a wave with 33 tokens).
@@ -186,6 +189,7 @@ constexpr int kDppRowRor = 0x120 + N;
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
+// (13 to 61 scalar values live in lanes of vector registers; nothing goes to memory.)
 // XREG: H has no more 512-column groups than there are waves, so that a wave's activations are the same for
 // all its tiles and stay in registers.
 template <bool LBF16, int EC, bool XREG>
@@ -387,9 +391,10 @@ constexpr int kDownEntries = kMaxE + kMaxT * MXFP4_MOE_MAX_TOP_K / kDownTokens;
 
 // RT: tiles of 16 rows that share a unit's activations.  RT = 1: one workgroup has all the units of its rows.
 // RT = 4, for several tokens per expert: the h of all tokens passes through every workgroup, so fewer, taller
-// ones read less of it (64 tokens, 8 of 64 experts, 4096 x 1536: 131 us with RT = 1); RT workgroups then share
+// ones read less of it (64 tokens, 8 of 64 experts, 4096 x 1536, with two planes: 131 us with RT = 1); RT workgroups then share
 // the units of 64 rows, each leaves its sums in the workspace, and the one that finishes last adds them in
-// order.
+// order.  The tall form needs eight registers more than there are and keeps them in memory, 28 bytes a lane: 3 of the 5.3
+// MiB that a launch for 33 tokens writes.
 template <class OT, int RT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
     extern __shared__ __align__(16) float sums[];  // [waves][T][16 RT]
@@ -509,7 +514,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
         }
     } else if (u0 < units) {
         // A unit's four tiles are enough to have one unit in flight ahead.  Refilling a chunk's registers as its
-        // products are done, as k_moe_up does, was no faster here: 33 tokens 148 -> 151 us, 1 token 27.0 -> 27.9 us.
+        // products are done, as k_moe_up does, was no faster here (with two planes): 33 tokens 148 -> 151 us, 1 token
+        // 27.0 -> 27.9 us.
         int tok = load_tok(u0);
         Tile w = load_w(u0);
         int u = u0;
@@ -639,8 +645,9 @@ hipError_t launch_mx_moe(const MoeArgs &p, void *workspace, int num_cus, hipStre
     a.tiles = a.I / 16;
     // Tiles per workgroup: an even share of one round over the device, at most 12.  Starting a workgroup costs about
     // as much as one tile, and long runs leave CUs without work in the last round.  Layers of 4096 x 1536, runs of 8,
-    // 12, 16 tiles at most: 4 tokens, 8 of 64 experts 82.8, 72.0, 72 us; 8 tokens 130, 128, 143 us; 33 tokens, 4 of
-    // 64 157, 152, 165 us; 64 tokens, 8 of 64 202, 207, 195 us.
+    // 12, 16 tiles at most, with two planes: 4 tokens, 8 of 64 experts 82.8, 72.0, 72 us; 8 tokens 130, 128, 143 us; 33
+    // tokens, 4 of 64 157, 152, 165 us; 64 tokens, 8 of 64 202, 207, 195 us.  Measured at H = 4096 only, which is also where
+    // the eight waves have a 512-column group each; with smaller H fewer of them work.
     a.tile_run = (int)std::min<int64_t>(12, std::max<int64_t>(1, ((int64_t)a.slots * a.tiles + num_cus - 1) / num_cus));
     a.runs = (a.tiles + a.tile_run - 1) / a.tile_run;
     const bool tall = a.T * a.k >= kTallTokens * a.E;
