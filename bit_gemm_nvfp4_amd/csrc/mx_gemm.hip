@@ -30,6 +30,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kSkinnyMaxM = 16;
+static_assert(bounds::kPastRange == kOffsetPastRange, "one offset past every range");
 static_assert(kPlanWindow == kGroup, "K slices are whole windows of scale bytes");
 
 template <class OT>
