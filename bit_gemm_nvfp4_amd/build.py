@@ -27,7 +27,8 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 SOURCES = ["api.hip", "quantize.hip", "dequantize.hip", "gemm.hip", "percentile.hip", "stats.hip", "lowrank.hip",
-           "mx_api.hip", "mx_codec.hip", "mx_gemm.hip", "mx_moe.hip"]
+           "mx_api.hip", "mx_codec.hip", "mx_gemm.hip", "mx_moe.hip", "mx_route.hip",
+           "mx_grouped.hip"]
 
 
 def _compile(src: str) -> str:

@@ -153,6 +153,23 @@ __device__ __forceinline__ void group_product(const MxGroup (&w)[RT], const Bf16
     }
 }
 
+// Eight fp32 values of a block of 32 that four neighbouring lanes (4 q .. 4 q + 3) hold between them -> the lane's codes
+// and the block's scale byte, as mxfp4_quantize makes them.
+__device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint32_t &b) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 8; q++) m = max(m, f2u(x[q]) & 0x7FFFFFFFu);
+    m = max(m, dpp_u32<kDppXor1>(m));
+    m = max(m, dpp_u32<kDppXor2>(m));
+    const uint32_t e = m >> 23;
+    b = e == 255 ? 255u : e > 2 ? e - 2 : 0;
+    const float inv = u2f((254u - (e > 2 ? e - 2 : 0)) << 23);
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; q++) v[q] = x[q] * inv;
+    return e == 255 ? 0u : fp4_pack8(v);
+}
+
 // Host side ---------------------------------------------------------------------------------------
 hipError_t launch_mx_quantize(const void *x, nvfp4_dtype dt, int64_t ld_x, const float *src_scale,
                               const mxfp4_tensor *out, int32_t *flags, hipStream_t stream);
@@ -181,5 +198,42 @@ struct MoeArgs {
     float *weights;
 };
 hipError_t launch_mx_moe(const MoeArgs &a, void *workspace, int num_cus, hipStream_t stream);
+
+
+// Router, sort by group, weighted sum (mx_route.hip).
+struct MxRouteArgs {
+    const void *logits;
+    bool logits_bf16;
+    int64_t tokens, ld_logits, experts;
+    int top_k, renormalize;
+    int32_t *ids;
+    float *weights;
+    int32_t *offsets, *rows, *places;
+};
+size_t mx_route_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts);
+hipError_t launch_mx_route(const MxRouteArgs &a, void *workspace, hipStream_t stream);
+size_t mx_sort_ws_bytes(int64_t pairs, int64_t groups);
+hipError_t launch_mx_sort(const int32_t *ids, int64_t rows, int per_row, int64_t groups, int32_t *offsets, int32_t *out_rows,
+                          int32_t *places, void *workspace, hipStream_t stream);
+hipError_t launch_mx_combine(const void *z, nvfp4_dtype z_dtype, int64_t z_rows, int64_t ld_z, const int32_t *places,
+                             const float *weights, int64_t tokens, int top_k, int64_t cols, void *y, nvfp4_dtype y_dtype,
+                             int64_t ld_y, hipStream_t stream);
+
+// Products grouped by rows (mx_grouped.hip): C [rows x N] or, with swiglu, [rows x N / 2].
+struct MxGroupedArgs {
+    const void *a_bf16;         // one of a_bf16 and a_q
+    const mxfp4_tensor *a_q;
+    int64_t a_rows, lda;
+    const int32_t *map;         // row of A of each row of C; null: the same
+    const int32_t *offsets;
+    int64_t groups, rows;
+    const mxfp4_tensor *w;      // [groups * N x K]
+    bool swiglu;
+    void *c;                    // one of c and c_q (with swiglu)
+    nvfp4_dtype c_dtype;
+    int64_t ldc;
+    const mxfp4_tensor *c_q;
+};
+hipError_t launch_mx_grouped(const MxGroupedArgs &a, int num_cus, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -88,4 +88,48 @@ inline MxPlan plan_mx_within(int64_t M, int64_t N, int64_t K, bool a_mx, int num
     return plan_ws_bytes(p, M, N) <= have ? p : plan_mx(M, N, K, a_mx, num_cus, 1);
 }
 
+// Products grouped by rows: the tile shapes, of 64 columns a wave each, and their costs as above.
+constexpr int kGroupShapes = 5;
+constexpr TileCost kGroupCost[2][kGroupShapes] = {
+    {{256, 256, 8, 1, 3.0, 12.6, 12.6},
+     {128, 256, 8, 1, 5.0, 6.4, 6.4},
+     {128, 128, 4, 2, 4.0, 4.0, 7.0},
+     {64, 128, 4, 2, 3.0, 2.8, 4.5},
+     {32, 128, 2, 4, 3.0, 2.1, 5.0}},
+    {{256, 256, 8, 1, 7.8, 3.84, 3.84},
+     {128, 256, 8, 1, 5.0, 2.4, 2.4},
+     {128, 128, 8, 1, 2.5, 1.5, 1.5},
+     {64, 128, 4, 2, 2.5, 1.05, 1.8},
+     {32, 128, 2, 4, 2.5, 0.9, 2.2}},
+};
+
+// Most tiles of `bm` rows that `rows` rows in `groups` groups can take: a last one that is not full per group with rows.
+inline int64_t group_tiles(int64_t rows, int64_t groups, int bm) {
+    return rows / bm + (groups < rows ? groups : rows);
+}
+
+// The cheapest shape for groups of about the same size, of which only the sum is known here; -1 when no launch holds
+// its tiles.  A group's last tile is half full on average.
+inline int plan_grouped(int64_t rows, int64_t groups, int64_t N, int64_t K, bool a_mx, int num_cus) {
+    const int64_t windows = (K + kPlanWindow - 1) / kPlanWindow;
+    int best = -1;
+    double cost = 1e30;
+    for (int cfg = 0; cfg < kGroupShapes; cfg++) {
+        const TileCost &t = kGroupCost[a_mx ? 1 : 0][cfg];
+        const int64_t tn = (N + t.bn - 1) / t.bn;
+        if ((uint64_t)tile_grid(group_tiles(rows, groups, t.bm) * tn) * 64 * t.waves > kMaxGridThreads) continue;
+        const double used = (double)(groups < rows ? groups : rows);
+        double tm = (double)rows / t.bm + used / 2;
+        if (tm < used) tm = used;
+        const double tiles = tm * (double)tn, slots = (double)num_cus * t.per_cu;
+        const double rounds = tiles <= slots ? 1.0 : tiles / slots;
+        const double us = tiles <= num_cus ? t.start + windows * t.window : rounds * (t.start + windows * t.window_full);
+        if (us < cost) {
+            cost = us;
+            best = cfg;
+        }
+    }
+    return best;
+}
+
 }  // namespace nvfp4

@@ -1,0 +1,422 @@
+// Router of a mixture-of-experts layer for any number of tokens, the sort of rows by group behind it, and the weighted
+// sum of what the groups give back (gfx950).
+//
+// k_mx_route: top-k choices and softmax weights of a row of logits, one wave per row: the row sits in registers as
+//   unsigned keys (mx_route.h) and gives its largest entry k times.
+// k_mx_count, k_mx_place: a counting sort of the (row, choice) pairs by group, stable in the pairs' order.  A
+//   workgroup has a run of pairs; its counts per group (k_mx_route makes them as it goes, k_mx_count for choices that
+//   are given) go to the workspace, and k_mx_place adds up those of the workgroups before its own, so that every pair's
+//   place follows from counts alone.  Nothing is made by atomics, so the order never depends on timing.  Up to
+//   kOneBlockRows rows one workgroup does both parts in one launch.
+// k_mx_combine: y[t] = sum_j w[t][j] z[places[t][j]] in fp32, in the order of j.  Bound by reading z.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "mx.h"
+#include "mx_route.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kMaxG = MXFP4_MOE_MAX_EXPERTS;
+constexpr int kWaves = 16, kThreads = 64 * kWaves;
+constexpr int kMaxBlocks = 256;      // runs of pairs
+constexpr int kOneBlockRows = 64;    // rows of logits that one workgroup routes and sorts
+constexpr int kOneBlockPairs = 4096; // given choices that one workgroup sorts
+
+struct RouteDev {
+    const void *logits;
+    int64_t ld;
+    int64_t T, P;
+    int E, k, renorm;
+    const int32_t *ids;  // the choices to sort
+    int32_t *out_ids;    // k_mx_route: where they are written (= ids)
+    float *weights;
+    int32_t *offsets, *rows, *places;
+    int32_t *hist;  // [blocks][E]
+    int blocks;
+    int64_t run;  // pairs per workgroup; whole rows for k_mx_route
+};
+
+struct SortShared {
+    uint32_t cnt[kWaves][kMaxG];
+    uint32_t tot[kThreads], pre[kThreads];
+    uint32_t wave_sum[kWaves];
+};
+
+// Lanes of the wave whose group is the lane's own (of the lanes with `ok`).
+__device__ __forceinline__ uint64_t same_group(int g, bool ok, int bits) {
+    uint64_t m = __ballot(ok);
+    for (int b = 0; b < bits; b++) {
+        const uint64_t set = __ballot(g >> b & 1);
+        m &= g >> b & 1 ? set : ~set;
+    }
+    return m;
+}
+
+// Sums over the waves of the counts of each group.
+__device__ __forceinline__ uint32_t group_count(const SortShared &s, int e) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) n += s.cnt[w][e];
+    return n;
+}
+
+// The wave's part of the workgroup's n pairs: whole batches of 64, so that waves hold consecutive runs.
+__device__ __forceinline__ void wave_part(int64_t n, int wave, int64_t &lo, int64_t &hi) {
+    const int64_t q = ((n + kWaves - 1) / kWaves + 63) / 64 * 64;
+    lo = min(n, wave * q);
+    hi = min(n, lo + q);
+}
+
+// Counts per wave and group of the workgroup's pairs n0 .. n0 + n - 1.  Lanes of one group let the first of them add.
+__device__ __forceinline__ void count_pairs(const RouteDev &a, SortShared &s, int64_t n0, int64_t n, int bits) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int j = tid; j < kWaves * a.E; j += kThreads) s.cnt[j / a.E][j % a.E] = 0;
+    __syncthreads();
+    int64_t lo, hi;
+    wave_part(n, wave, lo, hi);
+    for (int64_t i = lo; i < hi; i += 64) {
+        const int g = i + lane < hi ? a.ids[n0 + i + lane] : -1;
+        const bool ok = (unsigned)g < (unsigned)a.E;
+        const uint64_t m = same_group(g, ok, bits);
+        if (ok && lane == __builtin_ctzll(m)) s.cnt[wave][g] += __popcll(m);
+    }
+    __syncthreads();
+}
+
+// Places of the workgroup's pairs, whose counts are in s.cnt; offsets by workgroup 0.
+__device__ void place_pairs(const RouteDev &a, SortShared &s, int block, int64_t n0, int64_t n, int bits) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // totals of each group, and of the workgroups before this one: parts of the table's rows per thread
+    int width = 64;
+    while (width < a.E) width *= 2;
+    const int parts = kThreads / width, e = tid & (width - 1), part = tid / width;
+    uint32_t total = 0, before = 0;
+    if (a.blocks > 1 && e < a.E) {
+        const int per = (a.blocks + parts - 1) / parts, b1 = min(a.blocks, (part + 1) * per);
+        for (int b = part * per; b < b1; b++) {
+            const uint32_t v = (uint32_t)a.hist[(int64_t)b * a.E + e];
+            total += v;
+            before += b < block ? v : 0;
+        }
+    } else if (a.blocks == 1 && part == 0 && e < a.E) {
+        total = group_count(s, e);
+    }
+    s.tot[tid] = total;
+    s.pre[tid] = before;
+    __syncthreads();
+    total = before = 0;
+    if (tid < a.E) {
+        for (int p = 0; p < parts; p++) {
+            total += s.tot[p * width + tid];
+            before += s.pre[p * width + tid];
+        }
+    }
+    uint32_t upto = total;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t v = __shfl_up(upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 63) s.wave_sum[wave] = upto;
+    __syncthreads();
+    uint32_t first = upto - total, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+        if (w < wave) first += s.wave_sum[w];
+        all += s.wave_sum[w];
+    }
+    if (tid < a.E) {
+        if (block == 0) a.offsets[tid] = (int32_t)first;
+        uint32_t run = first + before;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) {
+            const uint32_t c = s.cnt[w][tid];
+            s.cnt[w][tid] = run;
+            run += c;
+        }
+    }
+    if (block == 0 && tid == 0) a.offsets[a.E] = (int32_t)all;
+    __syncthreads();
+    int64_t lo, hi;
+    wave_part(n, wave, lo, hi);
+    for (int64_t i = lo; i < hi; i += 64) {
+        const bool in = i + lane < hi;
+        const int g = in ? a.ids[n0 + i + lane] : -1;
+        const bool ok = (unsigned)g < (unsigned)a.E;
+        const uint64_t m = same_group(g, ok, bits);
+        int at = -1;
+        if (ok) {
+            const uint32_t base = s.cnt[wave][g];
+            at = (int)(base + __popcll(m & ((1ull << lane) - 1)));
+            if (lane == __builtin_ctzll(m)) s.cnt[wave][g] = base + __popcll(m);
+            a.rows[at] = (int32_t)((uint32_t)(n0 + i + lane) / (uint32_t)a.k);
+        }
+        if (in && a.places) a.places[n0 + i + lane] = at;
+    }
+    // positions behind the last group
+    for (int64_t i = all + (int64_t)block * kThreads + tid; i < a.P; i += (int64_t)a.blocks * kThreads) a.rows[i] = -1;
+}
+
+__device__ __forceinline__ int group_bits(int E) {
+    return 32 - __builtin_clz((unsigned)E);
+}
+
+// One row: the lane j < k gets choice j, its id and weight.  A row with a NaN or +infinity has no choices, and NaN for
+// weights.
+template <bool BF16, int EC>
+__device__ __forceinline__ void route_row(const RouteDev &a, int64_t t, int lane, int &id, float &w) {
+    RowKeys<EC> r = load_row_keys<BF16, EC>(a.logits, a.ld, a.E, t, lane);
+    const bool bad = row_bad(r);
+    const float top = key_to_f32(row_max(r));
+    float s = 0.0f;
+    if (!a.renorm) {
+#pragma unroll
+        for (int c = 0; c < EC; c++) s += r.k[c] > kKeyNegInf ? expf(key_to_f32(r.k[c]) - top) : 0.0f;
+    }
+    id = -1;
+    float p = 0.0f;
+    for (int j = 0; j < a.k && !bad; j++) {
+        uint32_t key;
+        const int e = pop_max(r, lane, key);
+        if (e < 0) break;
+        if (lane == j) {
+            id = e;
+            p = expf(key_to_f32(key) - top);
+        }
+    }
+    const float den = wave_sum_f32(a.renorm ? p : s);
+    w = bad ? __builtin_nanf("") : id >= 0 ? p / den : 0.0f;
+}
+
+template <bool BF16, int EC>
+__global__ __launch_bounds__(kThreads) void k_mx_route(RouteDev a) {
+    __shared__ SortShared s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t n0 = blockIdx.x * a.run, n = min(a.run, a.P - n0);
+    for (int j = tid; j < kWaves * a.E; j += kThreads) s.cnt[j / a.E][j % a.E] = 0;
+    __syncthreads();
+    const int64_t t1 = (n0 + n) / a.k;
+    for (int64_t t = n0 / a.k + wave; t < t1; t += kWaves) {
+        int id;
+        float w;
+        route_row<BF16, EC>(a, t, lane, id, w);
+        if (lane < a.k) {
+            a.out_ids[t * a.k + lane] = id;
+            a.weights[t * a.k + lane] = w;
+            if (id >= 0) s.cnt[wave][id]++;  // a row's choices differ, and no other wave has this line
+        }
+    }
+    __syncthreads();
+    if (a.blocks > 1) {
+        if (tid < a.E) a.hist[(int64_t)blockIdx.x * a.E + tid] = (int32_t)group_count(s, tid);
+        return;
+    }
+    const int bits = group_bits(a.E);
+    count_pairs(a, s, n0, n, bits);  // again by runs of pairs, the order of their places
+    place_pairs(a, s, 0, n0, n, bits);
+}
+
+__global__ __launch_bounds__(kThreads) void k_mx_count(RouteDev a) {
+    __shared__ SortShared s;
+    const int64_t n0 = blockIdx.x * a.run, n = min(a.run, a.P - n0);
+    count_pairs(a, s, n0, n, group_bits(a.E));
+    if ((int)threadIdx.x < a.E) a.hist[(int64_t)blockIdx.x * a.E + threadIdx.x] = (int32_t)group_count(s, threadIdx.x);
+}
+
+__global__ __launch_bounds__(kThreads) void k_mx_place(RouteDev a) {
+    __shared__ SortShared s;
+    const int64_t n0 = blockIdx.x * a.run, n = min(a.run, a.P - n0);
+    const int bits = group_bits(a.E);
+    count_pairs(a, s, n0, n, bits);
+    place_pairs(a, s, blockIdx.x, n0, n, bits);
+}
+
+// 16 bytes of a row of z as fp32 values.
+template <class T>
+struct Piece;
+template <>
+struct Piece<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void add(float w, u32x4 r, float *s) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) s[i] += w * u2f(r[i]);
+    }
+};
+template <>
+struct Piece<__bf16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void add(float w, u32x4 r, float *s) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t v = r[i];
+            s[2 * i] += w * u2f(v << 16);
+            s[2 * i + 1] += w * u2f(v & 0xFFFF0000u);
+        }
+    }
+};
+
+// Rows of y by blockIdx.y and up, a piece of 16 bytes of z per thread.  A last piece that ends behind the row's columns,
+// and rows of z (z_wide) or y (y_wide) that are not 16-byte aligned, go element by element.
+template <class ZT, class YT>
+__global__ __launch_bounds__(256) void k_mx_combine(const ZT *__restrict__ z, int64_t ld_z, int64_t z_rows,
+                                                    const int32_t *__restrict__ places, const float *__restrict__ weights,
+                                                    int64_t T, int k, int64_t cols, YT *__restrict__ y, int64_t ld_y,
+                                                    int z_wide, int y_wide) {
+    constexpr int N = Piece<ZT>::N;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;
+    if (c >= cols) return;
+    const int left = (int)min((int64_t)N, cols - c);
+    for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+        float s[N] = {};
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            u32x4 r[4];
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                r[j] = u32x4{0, 0, 0, 0};
+                w[j] = 0.0f;
+                if (j0 + j >= k) continue;
+                const int64_t at = places[t * k + j0 + j];
+                w[j] = weights[t * k + j0 + j];
+                if (at < 0 || at >= z_rows) continue;  // counts as a row of zeros
+                const ZT *p = z + at * ld_z + c;
+                if (z_wide && left == N) {
+                    r[j] = *reinterpret_cast<const u32x4 *>(p);
+                } else {
+                    ZT v[N] = {};
+#pragma unroll
+                    for (int i = 0; i < N; i++)
+                        if (i < left) v[i] = p[i];
+                    r[j] = *reinterpret_cast<const u32x4 *>(v);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) Piece<ZT>::add(w[j], r[j], s);
+        }
+        YT *dst = y + t * ld_y + c;
+        if (y_wide && left == N) {
+            constexpr int PER = 16 / sizeof(YT) < N ? 16 / sizeof(YT) : N;
+            typedef YT vec __attribute__((ext_vector_type(PER)));
+#pragma unroll
+            for (int q = 0; q < N / PER; q++) {
+                vec o;
+#pragma unroll
+                for (int i = 0; i < PER; i++) o[i] = (YT)s[q * PER + i];
+                *reinterpret_cast<vec *>(dst + q * PER) = o;
+            }
+        } else {
+            for (int i = 0; i < left; i++) dst[i] = (YT)s[i];
+        }
+    }
+}
+
+int64_t runs_of(int64_t n, int64_t least, int64_t &run) {
+    run = std::max<int64_t>(least, (n + kMaxBlocks - 1) / kMaxBlocks);
+    return (n + run - 1) / run;
+}
+
+// Workgroups and pairs per workgroup of a router's call, and of a sort of given choices.
+int64_t route_blocks(int64_t tokens, int top_k, int64_t &run) {
+    if (tokens <= kOneBlockRows) {
+        run = tokens * top_k;
+        return 1;
+    }
+    const int64_t blocks = runs_of(tokens, kWaves, run);
+    run *= top_k;
+    return blocks;
+}
+
+int64_t sort_blocks(int64_t pairs, int64_t &run) { return runs_of(pairs, kOneBlockPairs, run); }
+
+template <bool BF16>
+void launch_route_t(const RouteDev &a, hipStream_t stream) {
+    const dim3 grid((unsigned)a.blocks), block(kThreads);
+    if (a.E <= 64) hipLaunchKernelGGL((k_mx_route<BF16, 1>), grid, block, 0, stream, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((k_mx_route<BF16, 2>), grid, block, 0, stream, a);
+    else if (a.E <= 256) hipLaunchKernelGGL((k_mx_route<BF16, 4>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((k_mx_route<BF16, 8>), grid, block, 0, stream, a);
+}
+
+}  // namespace
+
+size_t mx_route_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
+    if (tokens <= 0 || top_k <= 0 || experts <= 0) return 0;
+    int64_t run;
+    const int64_t blocks = route_blocks(tokens, (int)top_k, run);
+    return blocks > 1 ? (size_t)(blocks * experts * 4) : 0;
+}
+
+size_t mx_sort_ws_bytes(int64_t pairs, int64_t groups) {
+    if (pairs <= 0 || groups <= 0) return 0;
+    int64_t run;
+    const int64_t blocks = sort_blocks(pairs, run);
+    return blocks > 1 ? (size_t)(blocks * groups * 4) : 0;
+}
+
+hipError_t launch_mx_route(const MxRouteArgs &p, void *workspace, hipStream_t stream) {
+    RouteDev a{};
+    a.logits = p.logits;
+    a.ld = p.ld_logits;
+    a.T = p.tokens;
+    a.P = p.tokens * p.top_k;
+    a.E = (int)p.experts;
+    a.k = p.top_k;
+    a.renorm = p.renormalize;
+    a.ids = a.out_ids = p.ids;
+    a.weights = p.weights;
+    a.offsets = p.offsets;
+    a.rows = p.rows;
+    a.places = p.places;
+    a.hist = reinterpret_cast<int32_t *>(workspace);
+    a.blocks = (int)route_blocks(p.tokens, p.top_k, a.run);
+    if (p.logits_bf16) launch_route_t<true>(a, stream);
+    else launch_route_t<false>(a, stream);
+    if (a.blocks > 1) hipLaunchKernelGGL(k_mx_place, dim3((unsigned)a.blocks), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_sort(const int32_t *ids, int64_t rows, int per_row, int64_t groups, int32_t *offsets, int32_t *out_rows,
+                          int32_t *places, void *workspace, hipStream_t stream) {
+    RouteDev a{};
+    a.T = rows;
+    a.P = rows * per_row;
+    a.E = (int)groups;
+    a.k = per_row;
+    a.ids = ids;
+    a.offsets = offsets;
+    a.rows = out_rows;
+    a.places = places;
+    a.hist = reinterpret_cast<int32_t *>(workspace);
+    a.blocks = (int)std::max<int64_t>(1, sort_blocks(a.P, a.run));  // without pairs: the offsets
+    if (a.blocks > 1) hipLaunchKernelGGL(k_mx_count, dim3((unsigned)a.blocks), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(k_mx_place, dim3((unsigned)a.blocks), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_combine(const void *z, nvfp4_dtype z_dtype, int64_t z_rows, int64_t ld_z, const int32_t *places,
+                             const float *weights, int64_t tokens, int top_k, int64_t cols, void *y, nvfp4_dtype y_dtype,
+                             int64_t ld_y, hipStream_t stream) {
+    const int per = z_dtype == NVFP4_F32 ? 4 : 8, yeb = y_dtype == NVFP4_F32 ? 4 : 2;
+    const int y_wide = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld_y * yeb % 16 == 0;
+    const int z_wide = reinterpret_cast<uintptr_t>(z) % 16 == 0 && ld_z * (16 / per) % 16 == 0;
+    const dim3 grid((unsigned)((cols + 256 * per - 1) / (256 * per)), (unsigned)std::min<int64_t>(tokens, 65535));
+#define MX_COMBINE(ZT, YT)                                                                                                \
+    hipLaunchKernelGGL((k_mx_combine<ZT, YT>), grid, dim3(256), 0, stream, reinterpret_cast<const ZT *>(z), ld_z, z_rows, \
+                       places, weights, tokens, top_k, cols, reinterpret_cast<YT *>(y), ld_y, z_wide, y_wide)
+    if (z_dtype == NVFP4_F32) {
+        if (y_dtype == NVFP4_F32) MX_COMBINE(float, float);
+        else MX_COMBINE(float, __bf16);
+    } else {
+        if (y_dtype == NVFP4_F32) MX_COMBINE(__bf16, float);
+        else MX_COMBINE(__bf16, __bf16);
+    }
+#undef MX_COMBINE
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,5 +1,6 @@
 """MXFP4 (E2M1 codes, one power-of-two E8M0 scale per 32 elements of a row): quantization, expansion,
-the product with MXFP4 weights and the mixture-of-experts layer for a few tokens.
+the product with MXFP4 weights, the mixture-of-experts layer for a few tokens, and products whose rows pick
+their weights: router, products grouped by expert, the layer for any number of tokens.
 
 A thin ctypes binding over the entry points of ``include/mxfp4.h``; the package re-exports its names.
 """
@@ -13,11 +14,14 @@ import torch
 from . import (_DT, _I32, _I64, _P, _SIGNATURES, _RESTYPES, _SZ, _check, _rows, _workspace, check_flags,
                load_library)
 
-MX_OP_GEMM_BF16, MX_OP_GEMM_MX, MX_OP_MOE = 0, 1, 2
+MX_OP_GEMM_BF16, MX_OP_GEMM_MX, MX_OP_MOE, MX_OP_ROUTE, MX_OP_GROUP_ROWS = 0, 1, 2, 3, 4
 MX_BLOCK = 32
 SKINNY_MAX_M = 16  # products of up to this many rows take no workspace
 MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 64, 512, 16
-MX_EXPORTED = ["mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_moe", "mxfp4_workspace_size"]
+GROUP_MAX_ROWS, MAX_GROUPS = 1 << 24, MOE_MAX_EXPERTS
+MX_EXPORTED = ["mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_moe", "mxfp4_workspace_size", "mxfp4_route",
+               "mxfp4_group_rows", "mxfp4_grouped_gemm", "mxfp4_combine", "mxfp4_experts",
+               "mxfp4_experts_workspace_size"]
 
 
 class CMXTensor(ctypes.Structure):
@@ -33,8 +37,15 @@ _SIGNATURES.update({
     "mxfp4_gemm": [_P, _PX, _I64, _I64, _PX, _P, _I32, _I64, _P, _SZ, _P],
     "mxfp4_moe": [_P, _I64, _I64, _P, _I32, _I64, _I64, _I32, _I32, _PX, _PX, _P, _I32, _I64, _P, _P, _P, _SZ, _P],
     "mxfp4_workspace_size": [_I32, _I64, _I64, _I64],
+    "mxfp4_route": [_P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "mxfp4_group_rows": [_P, _I64, _I32, _I64, _P, _P, _P, _P, _SZ, _P],
+    "mxfp4_grouped_gemm": [_P, _PX, _I64, _I64, _P, _P, _I64, _I64, _PX, _I32, _P, _I32, _I64, _PX, _P],
+    "mxfp4_combine": [_P, _I32, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I32, _I64, _P],
+    "mxfp4_experts": [_P, _I64, _I64, _P, _I32, _I64, _I64, _I32, _I32, _I32, _PX, _PX, _P, _I32, _I64, _P, _P, _P, _SZ,
+                      _P],
+    "mxfp4_experts_workspace_size": [_I64, _I64, _I32, _I64, _I64, _I32, _I32],
 })
-_RESTYPES["mxfp4_workspace_size"] = _SZ
+_RESTYPES["mxfp4_workspace_size"] = _RESTYPES["mxfp4_experts_workspace_size"] = _SZ
 
 
 @dataclass
@@ -238,4 +249,162 @@ def mx_moe(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_down
     _call("mxfp4_moe", dev, x.data_ptr(), t, ld_x, logits.data_ptr(), _DT[logits.dtype], ld_l, logits.shape[1], top_k,
           1 if renormalize else 0, ctypes.byref(w_gate_up.c()), ctypes.byref(w_down.c()), out.data_ptr(), dt, ld_y,
           _opt(ids, dev, "ids"), _opt(weights, dev, "weights"), _opt(workspace, dev, "workspace"), _nbytes(workspace))
+    return (out, ids, weights) if routing else out
+
+
+# ------------------------------------------------------------------------------------------------
+# products whose rows pick their weights
+# ------------------------------------------------------------------------------------------------
+@dataclass
+class Grouping:
+    """Rows sorted by group (an expert): group g has the positions offsets[g] .. offsets[g + 1] - 1 (int32 [groups + 1]);
+    rows [tokens * per_token] int32 is the token at each position, -1 behind the last group's; places [tokens,
+    per_token] int32 the position of each choice, -1 where there is none.  From mx_route also the choices: ids [tokens,
+    top_k] int32 and their weights fp32."""
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    places: torch.Tensor | None = None
+    ids: torch.Tensor | None = None
+    weights: torch.Tensor | None = None
+
+
+def _words(t: torch.Tensor, what: str, device: torch.device, dtype: torch.dtype, *shape) -> int:
+    """Address of a dense tensor argument of the given type and shape."""
+    assert t.device == device and t.dtype is dtype and tuple(t.shape) == shape and t.is_contiguous(), \
+        f"{what}: a dense {dtype} tensor {shape} on {device} is required, not {tuple(t.shape)} {t.dtype} on {t.device}"
+    return t.data_ptr()
+
+
+def mx_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
+             workspace: torch.Tensor | None = None) -> Grouping:
+    """The router of a mixture-of-experts layer: the top_k largest of each row of logits [T, E] (fp32 or bf16; ties to
+    the lowest expert, -inf masks an expert), their softmax weights (over the chosen logits, or with renormalize=False
+    over all of the row's), and the tokens sorted by expert, in their order within an expert.  A row with a NaN or +inf
+    chooses no expert and has NaN weights."""
+    dev = logits.device
+    assert logits.dtype in (torch.float32, torch.bfloat16), f"logits: fp32 or bf16, not {logits.dtype}"
+    ld = _rows(logits, "logits")
+    t, e = logits.shape
+    assert top_k >= 1, f"top_k: at least 1, not {top_k}"
+    n = t * top_k
+    words = torch.empty(3 * n + e + 1, dtype=torch.int32, device=dev)  # one allocation
+    ids, places, rows, offsets = words[:n].view(t, top_k), words[n:2 * n].view(t, top_k), words[2 * n:3 * n], words[3 * n:]
+    weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _workspace(mx_workspace_size(MX_OP_ROUTE, t, top_k, e), dev)
+    _call("mxfp4_route", dev, logits.data_ptr(), _DT[logits.dtype], t, ld, e, top_k, 1 if renormalize else 0, ids.data_ptr(),
+          weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), places.data_ptr(), _opt(workspace, dev, "workspace"),
+          _nbytes(workspace))
+    return Grouping(offsets, rows, places, ids, weights)
+
+
+def mx_group_rows(ids: torch.Tensor, groups: int, workspace: torch.Tensor | None = None) -> Grouping:
+    """Sort tokens by the groups that they name: ids int32 [T, per_token] (or [T]) in 0 .. groups - 1, any other value
+    being no choice.  A token may name a group more than once."""
+    assert ids.is_cuda and ids.dtype is torch.int32 and ids.dim() in (1, 2) and ids.is_contiguous(), \
+        "ids: a dense int32 device tensor [tokens] or [tokens, per_token] is required"
+    t, per = ids.shape[0], 1 if ids.dim() == 1 else ids.shape[1]
+    dev = ids.device
+    offsets = torch.empty(max(groups, 0) + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(t * per, dtype=torch.int32, device=dev)
+    places = torch.empty((t, per), dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = _workspace(mx_workspace_size(MX_OP_GROUP_ROWS, t, per, groups), dev)
+    _call("mxfp4_group_rows", dev, ids.data_ptr(), t, per, groups, offsets.data_ptr(), rows.data_ptr(), places.data_ptr(),
+          _opt(workspace, dev, "workspace"), _nbytes(workspace))
+    return Grouping(offsets, rows, places)
+
+
+def mx_grouped_gemm(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                    swiglu: bool = False, dtype: torch.dtype = torch.float32,
+                    out: torch.Tensor | MXFP4Tensor | None = None) -> torch.Tensor | MXFP4Tensor:
+    """Products grouped by expert, of any sizes: for offsets[g] <= i < offsets[g + 1] (int32 [groups + 1], on the
+    device), C[i] = A[rows[i]] . W[g]^T, or with swiglu silu(A[rows[i]] . Wg[g]^T) * (A[rows[i]] . Wu[g]^T).
+
+    a: MXFP4Tensor (W4A4) or bf16 [R, K] (W4A16); rows: int32, the row of A of each row of C (all of A's, in order,
+    without it; one outside A counts as zeros); w [groups * N, K], groups stacked (swiglu: N / 2 gate rows, then N / 2 up
+    rows, per group).  Returns C [len(rows) or R, N or N / 2], fp32 or bf16; with swiglu `out` may be an MXFP4Tensor, which
+    is quantized from the fp32 values.  Rows outside every group are left as they are in `out`."""
+    assert isinstance(w, MXFP4Tensor), "w: an MXFP4Tensor is required"
+    wr, k = w.shape
+    dev = w.codes.device
+    assert offsets.dim() == 1 and offsets.numel() >= 2, f"offsets: [groups + 1] is required, not {tuple(offsets.shape)}"
+    groups = offsets.numel() - 1
+    parts = groups * (2 if swiglu else 1)
+    assert wr % parts == 0, f"w: {wr} rows do not make {groups} groups"
+    n = wr // parts
+    if isinstance(a, MXFP4Tensor):
+        assert a.shape[1] == k and a.codes.device == dev, f"a: {a.shape} on {a.codes.device}, expected {k} columns on {dev}"
+        a_ct, a_ptr, lda = ctypes.byref(a.c()), None, k
+    else:
+        assert isinstance(a, torch.Tensor) and a.dtype is torch.bfloat16 and a.device == dev, \
+            f"a: a bf16 tensor or an MXFP4Tensor on {dev} is required"
+        lda = _rows(a, "a", k)
+        a_ct, a_ptr = None, a.data_ptr()
+    m = a.shape[0] if rows is None else rows.numel()
+    map_ptr = None if rows is None else _words(rows, "rows", dev, torch.int32, m)
+    off_ptr = _words(offsets, "offsets", dev, torch.int32, groups + 1)
+    if isinstance(out, MXFP4Tensor):
+        assert swiglu and out.shape == (m, n) and out.codes.device == dev, \
+            f"out: MXFP4 {out.shape} on {out.codes.device}, expected {(m, n)} on {dev}, with swiglu"
+        c_ct, c_ptr, ldc, dt = ctypes.byref(out.c()), None, n, 0
+    else:
+        out, ldc, dt = _out(out, m, n, dtype, dev, "out")
+        c_ct, c_ptr = None, out.data_ptr()
+    _call("mxfp4_grouped_gemm", dev, a_ptr, a_ct, a.shape[0], lda, map_ptr, off_ptr, groups, m, ctypes.byref(w.c()),
+          1 if swiglu else 0, c_ptr, dt, ldc, c_ct)
+    return out
+
+
+def mx_combine(z: torch.Tensor, places: torch.Tensor, weights: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] z[places[t, j]] (fp32 sums in the order of j): what a token's choices gave back.  z [P, N]
+    fp32 or bf16; places int32 and weights fp32 [T, top_k]; a place outside z counts as a row of zeros."""
+    assert z.dtype in (torch.float32, torch.bfloat16), f"z: fp32 or bf16, not {z.dtype}"
+    dev = z.device
+    ld = _rows(z, "z")
+    assert places.dim() == 2, f"places: [tokens, top_k] is required, not {tuple(places.shape)}"
+    t, k = places.shape
+    cols = z.shape[1]
+    out, ld_y, dt = _out(out, t, cols, dtype, dev, "out")
+    _call("mxfp4_combine", dev, z.data_ptr(), _DT[z.dtype], z.shape[0], ld, _words(places, "places", dev, torch.int32, t, k),
+          _words(weights, "weights", dev, torch.float32, t, k), t, k, cols, out.data_ptr(), dt, ld_y)
+    return out
+
+
+def mx_experts_workspace(tokens: int, experts: int, top_k: int, w_gate_up: MXFP4Tensor, w_down: MXFP4Tensor,
+                         quantize_acts: bool = True, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor | None:
+    """A workspace for mx_experts (None without tokens).  Its contents do not matter; calls that share one must be ordered
+    (same stream, or events)."""
+    nbytes = int(load_library().mxfp4_experts_workspace_size(tokens, experts, top_k, w_gate_up.shape[1], w_down.shape[1],
+                                                             1 if quantize_acts else 0, _DT[dtype]))
+    return _workspace(nbytes, w_down.codes.device)
+
+
+def mx_experts(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_down: MXFP4Tensor, top_k: int,
+               renormalize: bool = True, quantize_acts: bool = True, dtype: torch.dtype = torch.bfloat16,
+               routing: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """The mixture-of-experts layer of mx_moe for any number of tokens (a prompt, a large batch): router, grouped
+    products and weighted sum.  With quantize_acts x and silu(gate) * up go through MXFP4 (W4A4), else through bf16 (W4A16);
+    what an expert gives a token is rounded to y's type before the weighted fp32 sum.  mx_moe keeps more bits and is
+    faster for few tokens.  Arguments, layouts and returns as for mx_moe (a row with NaN or +inf has NaN weights)."""
+    dev = x.device
+    assert x.dtype is torch.bfloat16, f"x: bf16, not {x.dtype}"
+    assert logits.dtype in (torch.float32, torch.bfloat16), f"logits: fp32 or bf16, not {logits.dtype}"
+    ld_x, ld_l = _rows(x, "x", w_gate_up.shape[1]), _rows(logits, "logits")
+    t, h = x.shape
+    assert logits.shape[0] == t, f"logits: {logits.shape[0]} rows, expected {t}"
+    assert logits.device == dev and w_gate_up.codes.device == dev and w_down.codes.device == dev, "one device per call"
+    out, ld_y, dt = _out(out, t, h, dtype, dev, "out")
+    ids = weights = None
+    if routing:
+        ids = torch.empty((t, top_k), dtype=torch.int32, device=dev)
+        weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+    e = logits.shape[1]
+    if workspace is None:
+        workspace = mx_experts_workspace(t, e, top_k, w_gate_up, w_down, quantize_acts, out.dtype)
+    _call("mxfp4_experts", dev, x.data_ptr(), t, ld_x, logits.data_ptr(), _DT[logits.dtype], ld_l, e, top_k,
+          1 if renormalize else 0, 1 if quantize_acts else 0, ctypes.byref(w_gate_up.c()), ctypes.byref(w_down.c()),
+          out.data_ptr(), dt, ld_y, _opt(ids, dev, "ids"), _opt(weights, dev, "weights"), _opt(workspace, dev, "workspace"),
+          _nbytes(workspace))
     return (out, ids, weights) if routing else out

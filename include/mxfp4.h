@@ -1,7 +1,8 @@
 /*
  * mxfp4.h -- MXFP4 entry points of libnvfp4.so: block quantization with power-of-two scales, its
- * expansion, the product with MXFP4 weights and a mixture-of-experts layer for a few tokens, as
- * hand-written HIP kernels for AMD Instinct MI355X (gfx950).
+ * expansion, the product with MXFP4 weights, a mixture-of-experts layer for a few tokens, and products whose
+ * rows pick their weights (router, products grouped by expert, the layer for any number of tokens, adapters
+ * per request), as hand-written HIP kernels for AMD Instinct MI355X (gfx950).
  *
  * MXFP4 (OCP Microscaling Formats, MXFP4): E2M1 codes as in nvfp4.h (magnitudes {0, 0.5, 1, 1.5, 2,
  * 3, 4, 6} and a sign bit, element 2j of a row in the low nibble of byte j), and one E8M0 byte b per
@@ -38,7 +39,9 @@ typedef struct {
 enum {
     MXFP4_OP_GEMM_BF16 = 0, /* mxfp4_gemm with bf16 activations: (M, N, K)                     */
     MXFP4_OP_GEMM_MX = 1,   /* mxfp4_gemm with MXFP4 activations: (M, N, K)                    */
-    MXFP4_OP_MOE = 2        /* mxfp4_moe: (tokens * top_k, H, I)                               */
+    MXFP4_OP_MOE = 2,       /* mxfp4_moe: (tokens * top_k, H, I)                               */
+    MXFP4_OP_ROUTE = 3,     /* mxfp4_route: (tokens, top_k, experts)                           */
+    MXFP4_OP_GROUP_ROWS = 4 /* mxfp4_group_rows: (tokens, per_token, groups)                   */
 };
 
 /* Largest arguments of mxfp4_moe. */
@@ -114,6 +117,94 @@ nvfp4_status mxfp4_moe(const void *x, int64_t tokens, int64_t ld_x, const void *
                        int64_t ld_logits, int64_t experts, int top_k, int renormalize, const mxfp4_tensor *w_gate_up,
                        const mxfp4_tensor *w_down, void *y, nvfp4_dtype y_dtype, int64_t ld_y, int32_t *ids,
                        float *weights, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Largest arguments of the entry points below: (row, choice) pairs or grouped rows, and groups. */
+enum { MXFP4_GROUP_MAX_ROWS = 1 << 24, MXFP4_MAX_GROUPS = MXFP4_MOE_MAX_EXPERTS };
+
+/*
+ * mxfp4_route -- the router of a mixture-of-experts layer, for any number of tokens: choices, weights and the
+ * order of the rows that the products grouped by expert take.
+ *   logits, renormalize   as for mxfp4_moe; logits [tokens x experts] fp32 or bf16, element-aligned rows
+ *   ids      [tokens x top_k]: the chosen experts in descending order of logit, ties to the lowest expert;
+ *            -1 where a row has fewer
+ *   weights  [tokens x top_k]: their softmax weights; 0 where a row has fewer.  A row with a NaN or +infinity
+ *            chooses no expert and has NaN for all its weights
+ *   offsets  [experts + 1]: expert e has the positions offsets[e] .. offsets[e + 1] - 1
+ *   rows     [tokens * top_k]: the token at each position, in the order of the tokens within an expert; -1 behind
+ *            the last expert's
+ *   places   [tokens x top_k]: the position of each choice, -1 where there is none
+ * All outputs are required, dense and 4-byte aligned.  The result does not depend on the order of execution.
+ * Errors: NVFP4_ERR_SHAPE for tokens * top_k > MXFP4_GROUP_MAX_ROWS, experts < 1 or > MXFP4_MAX_GROUPS, top_k >
+ * MXFP4_MOE_MAX_TOP_K; NVFP4_ERR_ARG for top_k < 1, top_k > experts or a bad renormalize; NVFP4_ERR_WORKSPACE for less
+ * than mxfp4_workspace_size(MXFP4_OP_ROUTE, tokens, top_k, experts) bytes (16-byte aligned; none for few tokens).
+ */
+nvfp4_status mxfp4_route(const void *logits, nvfp4_dtype logits_dtype, int64_t tokens, int64_t ld_logits, int64_t experts,
+                         int top_k, int renormalize, int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
+                         int32_t *places, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * mxfp4_group_rows -- the sort of mxfp4_route for choices that are given: ids [tokens x per_token] (dense) in 0 ..
+ * groups - 1; any other value is no choice.  A token may name a group more than once.  places may be NULL.  Outputs,
+ * limits (tokens * per_token, groups) and errors as for mxfp4_route; per_token >= 1 (NVFP4_ERR_ARG).
+ */
+nvfp4_status mxfp4_group_rows(const int32_t *ids, int64_t tokens, int per_token, int64_t groups, int32_t *offsets,
+                              int32_t *rows, int32_t *places, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/*
+ * mxfp4_grouped_gemm -- products whose rows are grouped: for every group g and offsets[g] <= i < offsets[g + 1]
+ *   C[i] = A[map[i]] . W[g]^T                                              (swiglu = 0), or
+ *   C[i] = silu(A[map[i]] . Wg[g]^T) * (A[map[i]] . Wu[g]^T)               (swiglu = 1)
+ * with silu(a) = a / (1 + exp(-a)).
+ *   a_bf16 [a_rows x K] bf16 (row stride lda) or a_q, MXFP4 [a_rows x K]: exactly one (NVFP4_ERR_ARG otherwise)
+ *   map      [rows] row of A of each row of C, or NULL for row i (then a_rows == rows).  A row outside 0 .. a_rows
+ *            - 1 counts as zeros.
+ *   offsets  [groups + 1] ascending.  They are read on the device; values outside 0 .. rows are cut off there.
+ *   w        [groups * N x K] MXFP4, groups stacked by rows; with swiglu a group's rows are N / 2 gate rows, then N / 2
+ *            up rows
+ *   c        [rows x N] (swiglu: N / 2) fp32 or bf16, row stride ldc; or c_q, an MXFP4 tensor of that shape (swiglu
+ *            only), as mxfp4_quantize makes it from the fp32 values.  Exactly one.
+ * Sums and silu are fp32, rounded once to C.  A group may be empty; rows of C outside every group are left as they are.
+ * W4A16 and W4A4 as for mxfp4_gemm.  No workspace.
+ * Errors: NVFP4_ERR_SHAPE for rows or a_rows > MXFP4_GROUP_MAX_ROWS, groups < 1 or > MXFP4_MAX_GROUPS, K == 0, K or
+ * lda above 2^20, w->rows not a multiple of groups (with swiglu: of 2 groups), N above 2^24, with a map a_rows rows of A
+ * of 2^31 bytes or more, with swiglu N / 2 rows of W of 2^30 bytes or more, or operands that disagree.
+ */
+nvfp4_status mxfp4_grouped_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t a_rows, int64_t lda, const int32_t *map,
+                                const int32_t *offsets, int64_t groups, int64_t rows, const mxfp4_tensor *w, int swiglu,
+                                void *c, nvfp4_dtype c_dtype, int64_t ldc, const mxfp4_tensor *c_q, hipStream_t stream);
+
+/*
+ * mxfp4_combine -- y[t] = sum_j weights[t][j] . z[places[t][j]]: the rows that a token's choices gave back, weighted, in
+ * the order of j.  z [z_rows x cols] fp32 or bf16 (row stride ld_z), places and weights [tokens x top_k] dense, y
+ * [tokens x cols] fp32 or bf16 (row stride ld_y).  Sums are fp32, rounded once.  A place outside 0 .. z_rows - 1 counts
+ * as a row of zeros, so a NaN weight still gives NaN.  Rows of z need the alignment of their element only.  top_k >= 1 (NVFP4_ERR_ARG), tokens * top_k <=
+ * MXFP4_GROUP_MAX_ROWS (NVFP4_ERR_SHAPE).
+ */
+nvfp4_status mxfp4_combine(const void *z, nvfp4_dtype z_dtype, int64_t z_rows, int64_t ld_z, const int32_t *places,
+                           const float *weights, int64_t tokens, int top_k, int64_t cols, void *y, nvfp4_dtype y_dtype,
+                           int64_t ld_y, hipStream_t stream);
+
+/*
+ * mxfp4_experts -- the mixture-of-experts layer of mxfp4_moe for any number of tokens: mxfp4_route, the gate and up
+ * product with its silu, the down product and mxfp4_combine, in the order of those calls.  Arguments as for mxfp4_moe;
+ * in between
+ *   quantize_acts = 1  x and h = silu(g) * u are quantized to MXFP4 (W4A4), h from its fp32 value;
+ *   quantize_acts = 0  x stays bf16 and h is rounded to bf16 (W4A16).
+ * What an expert gives a token is rounded to y's type, then weighted and summed in fp32.  (mxfp4_moe keeps more bits
+ * between its products and reads the weights of a few tokens' experts faster.)  ids, weights: optional, as mxfp4_route's.
+ * A row with a NaN or +infinity among its logits gives y = NaN.
+ * Errors as for mxfp4_moe, without its limit on tokens, and as for the calls named: tokens * top_k <=
+ * MXFP4_GROUP_MAX_ROWS, H and I <= 2^20, ld_x <= 2^20, x below 2^31 bytes; NVFP4_ERR_WORKSPACE for less than
+ * mxfp4_experts_workspace_size(...) bytes (16-byte aligned).
+ */
+nvfp4_status mxfp4_experts(const void *x, int64_t tokens, int64_t ld_x, const void *logits, nvfp4_dtype logits_dtype,
+                           int64_t ld_logits, int64_t experts, int top_k, int renormalize, int quantize_acts,
+                           const mxfp4_tensor *w_gate_up, const mxfp4_tensor *w_down, void *y, nvfp4_dtype y_dtype,
+                           int64_t ld_y, int32_t *ids, float *weights, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+size_t mxfp4_experts_workspace_size(int64_t tokens, int64_t experts, int top_k, int64_t H, int64_t I, int quantize_acts,
+                                    nvfp4_dtype y_dtype);
 
 /* Workspace bytes of an entry point (0 when none); see the selectors for the arguments.  Planned for
  * the current device (an MI355X's 256 CUs when none can be queried). */
