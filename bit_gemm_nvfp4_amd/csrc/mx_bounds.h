@@ -42,12 +42,12 @@ MX_BOTH uint32_t lane_off(uint32_t row_off, int col, int at, int row_len) {
     return col + at < row_len ? row_off + (uint32_t)at : kPastRange;
 }
 
-// The two parts of lane_off where each lane's row is its own: the offset of byte `at` of row `row` (-1: none), and the
-// bit that carries a step past the end of its rows beyond every range.
+// The two parts of lane_off where each lane's row is its own: the offset of byte `at` of row `row` (-1: none), and that
+// offset at a step whose columns start at byte `col`: past every range where the row ends before it.
 MX_BOTH uint32_t row_off(int row, int row_bytes, int at) {
     return row < 0 ? kPastRange : (uint32_t)row * (uint32_t)row_bytes + (uint32_t)at;
 }
-MX_BOTH uint32_t past_row(int col, int at, int row_len) { return col + at < row_len ? 0 : kPastRange; }
+MX_BOTH uint32_t step_off(uint32_t off, int col, int at, int row_len) { return col + at < row_len ? off : kPastRange; }
 
 }  // namespace bounds
 }  // namespace nvfp4

@@ -176,11 +176,12 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     auto load_stage = [&](int s) {
         uint8_t *dst = lds + (s % T::NST) * T::STAGE + wave * 1024;
         const int ao = s * T::A_ROWB, wo = s * T::W_ROWB;
-        const uint32_t aend = bounds::past_row(ao, apb, alen), wend = bounds::past_row(wo, wpb, wrb);
         const uint32_t as = bounds::part_soff(ao, abytes), ws = bounds::part_soff(wo, wbytes);
 #pragma unroll
         for (int i = 0; i < T::UPW; i++)
-            load_to_lds16(i < A_PER ? ra : rw, dst + i * (T::NW * 1024), off[i] | (i < A_PER ? aend : wend), i < A_PER ? as : ws);
+            load_to_lds16(i < A_PER ? ra : rw, dst + i * (T::NW * 1024),
+                          i < A_PER ? bounds::step_off(off[i], ao, apb, alen) : bounds::step_off(off[i], wo, wpb, wrb),
+                          i < A_PER ? as : ws);
     };
     const uint8_t *srow[T::SC_PER];
 #pragma unroll

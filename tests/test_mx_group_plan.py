@@ -116,7 +116,7 @@ static void lane(ll row, ll have, int rowb, int bk_steps, int nst, ll row_bytes,
     for (int s = 0; s < bk_steps + nst; s = s == 1 && bk_steps > 6 ? bk_steps - 3 : s + 1)
         for (int at = 0; at < rowb; at += 16) {
             const ll col = (ll)s * rowb + at;
-            const uint32_t off = row_off((int)row, (int)row_bytes, at) | past_row(s * rowb, at, (int)row_len);
+            const uint32_t off = step_off(row_off((int)row, (int)row_bytes, at), s * rowb, at, (int)row_len);
             load(bytes, off, part_soff((uint32_t)(s * rowb), (uint32_t)bytes),
                  row >= 0 && col < row_len ? row * row_bytes + col : -1);
         }
