@@ -500,6 +500,6 @@ def matrix_stats(w: torch.Tensor, q: NVFP4Tensor | None = None, out: torch.Tenso
 
 
 # MXFP4 entry points (include/mxfp4.h)
-from .mx import (Grouping, MX_EXPORTED, MXFP4Tensor, mx_combine, mx_dequantize, mx_experts,  # noqa: E402
-                 mx_experts_workspace, mx_gemm, mx_gemm_workspace, mx_group_rows, mx_grouped_gemm, mx_moe,
-                 mx_moe_workspace, mx_quantize, mx_route, mx_workspace_size)
+from .mx import (Grouping, MX_EXPORTED, MXFP4Tensor, mx_adapters_workspace, mx_combine, mx_dequantize,  # noqa: E402
+                 mx_experts, mx_experts_workspace, mx_gemm, mx_gemm_adapters, mx_gemm_workspace, mx_group_rows,
+                 mx_grouped_gemm, mx_moe, mx_moe_workspace, mx_quantize, mx_route, mx_workspace_size)

@@ -28,7 +28,7 @@ FLAGS = [
 ]
 SOURCES = ["api.hip", "quantize.hip", "dequantize.hip", "gemm.hip", "percentile.hip", "stats.hip", "lowrank.hip",
            "mx_api.hip", "mx_codec.hip", "mx_gemm.hip", "mx_moe.hip", "mx_route.hip",
-           "mx_grouped.hip"]
+           "mx_grouped.hip", "mx_adapters.hip"]
 
 
 def _compile(src: str) -> str:

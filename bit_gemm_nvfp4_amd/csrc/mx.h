@@ -180,7 +180,7 @@ hipError_t launch_mx_dequantize(const mxfp4_tensor *in, void *out, nvfp4_dtype o
 size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus);
 hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                           void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,
-                          int num_cus, hipStream_t stream);
+                          int num_cus, hipStream_t stream, const struct Adapters *ad = nullptr);
 
 size_t mx_moe_ws_bytes(int64_t pairs, int64_t hidden, int64_t inter);
 struct MoeArgs {

@@ -5,6 +5,7 @@
 
 #include "internal.h"
 #include "mx.h"
+#include "mx_adapters.h"
 #include "mxfp4.h"
 
 #include <initializer_list>
@@ -69,6 +70,11 @@ nvfp4_status first_of(std::initializer_list<nvfp4_status> all) {
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+// T at the front of the workspace of mxfp4_gemm_adapters.
+size_t adapters_t_bytes(int64_t M, int64_t rank) { return align256((size_t)M * rank * 4); }
+
+bool rank_fits(int64_t rank) { return rank >= 8 && rank <= MXFP4_MAX_RANK && rank % 8 == 0; }
 
 // Parts of the workspace of mxfp4_experts, each 256-byte aligned.
 struct ExpertsWs {
@@ -392,6 +398,54 @@ nvfp4_status mxfp4_experts(const void *x, int64_t tokens, int64_t ld_x, const vo
     e = launch_mx_grouped(down, cus, stream);
     if (e != hipSuccess) return launched(e);
     return launched(launch_mx_combine(ws + at.z, y_dtype, pairs, H, words(at.places), wts, tokens, top_k, H, y, y_dtype, ld_y, stream));
+}
+
+size_t mxfp4_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int quantized_acts) {
+    if (M <= 0 || M > MXFP4_GROUP_MAX_ROWS || N <= 0 || N > kMaxDim || K <= 0 || K > kMaxDim || !rank_fits(rank)) return 0;
+    const int cus = current_device_cus();
+    return adapters_t_bytes(M, rank) + mx_gemm_ws_bytes(M, N, K, quantized_acts != 0, cus > 0 ? cus : 256);
+}
+
+nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+                                 const int32_t *index, int64_t adapters, int64_t rank, const void *down, const void *up,
+                                 const float *scales, void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    nvfp4_status st = check_mx(w);
+    if (st != NVFP4_OK) return st;
+    const int64_t N = w->rows, K = w->cols;
+    if (c_dtype != NVFP4_F32 && c_dtype != NVFP4_BF16) return NVFP4_ERR_DTYPE;
+    if (M < 0 || M > MXFP4_GROUP_MAX_ROWS || K > kMaxK || (M > 16 && N > kMaxTileDim) || adapters < 0 ||
+        adapters > MXFP4_MAX_ADAPTERS || !rank_fits(rank))
+        return NVFP4_ERR_SHAPE;
+    st = check_rows(a_bf16, M, K, lda, 2, 16);
+    if (st != NVFP4_OK) return st;
+    if (M > 16 && lda > kMaxTileLd) return NVFP4_ERR_SHAPE;
+    if (a_q) {
+        st = check_mx(a_q);
+        if (st != NVFP4_OK) return st;
+        if (a_q->rows != M || a_q->cols != K) return NVFP4_ERR_SHAPE;
+    }
+    const int eb = elem_bytes(c_dtype);
+    st = first_of({check_rows(down, adapters * rank, K, K, 2, 16), check_rows(up, adapters, N * rank, N * rank, 2, 16),
+                   check_rows(c, M, N, ldc, eb, eb), check_words(index, M > 0), check_words(scales, false)});
+    if (st != NVFP4_OK) return st;
+    if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+    const size_t t_bytes = adapters_t_bytes(M, rank), have = workspace ? workspace_bytes : 0;
+    const bool branch = M > 0 && N > 0 && K > 0 && adapters > 0;
+    if (branch && have < t_bytes) return NVFP4_ERR_WORKSPACE;
+    const int cus = current_device_cus();
+    if (cus == 0) return NVFP4_ERR_DEVICE;
+    if (M == 0 || N == 0) return NVFP4_OK;
+    const Adapters ad{reinterpret_cast<const float *>(workspace), reinterpret_cast<const __bf16 *>(up), index, (int)adapters,
+                      (int)rank};
+    if (branch) {
+        const AdapterDownArgs d{a_bf16, M, lda, K, down, scales, index, (int)adapters, (int)rank, reinterpret_cast<float *>(workspace)};
+        const hipError_t e = launch_adapter_down(d, cus, stream);
+        if (e != hipSuccess) return launched(e);
+    }
+    uint8_t *planes = have > t_bytes ? reinterpret_cast<uint8_t *>(workspace) + t_bytes : nullptr;
+    return launched(launch_mx_gemm(a_q ? nullptr : a_bf16, a_q, M, lda, w, c, c_dtype, ldc, planes, planes ? have - t_bytes : 0,
+                                   cus, stream, branch ? &ad : nullptr));
 }
 
 }  // extern "C"

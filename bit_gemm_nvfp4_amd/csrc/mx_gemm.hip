@@ -45,13 +45,13 @@ constexpr int kStageRow = kGroup * 2 + 16;
 // MR = 0: MXFP4 activations, a quarter of that, read straight; the next W group's loads are issued before the
 // current one's products, into a second set of registers (copied from one set, the copies wait for the loads first: 1 x
 // 4096 x 12288 7.5 -> 7.2 us).  The other loop is no faster there (13 x 4096 x 12288 8.9 us, with it 9.8).
-template <int RT, int MR, class OT>
-__global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A, int64_t lda,
-                                                   const uint8_t *__restrict__ acodes,
-                                                   const uint8_t *__restrict__ ascales, int M,
-                                                   const uint8_t *__restrict__ wcodes,
-                                                   const uint8_t *__restrict__ wscales, int64_t N, int K, int stages,
-                                                   OT *__restrict__ C, int64_t ldc) {
+// branch(m, n, s): what becomes of the sum s of an element of C before it is rounded.
+template <int RT, int MR, class OT, class Branch>
+__device__ __forceinline__ void skinny_product(const __bf16 *__restrict__ A, int64_t lda,
+                                               const uint8_t *__restrict__ acodes, const uint8_t *__restrict__ ascales,
+                                               int M, const uint8_t *__restrict__ wcodes,
+                                               const uint8_t *__restrict__ wscales, int64_t N, int K, int stages,
+                                               OT *__restrict__ C, int64_t ldc, Branch branch) {
     extern __shared__ __align__(16) float red[];  // [waves][RT][256], then [waves][stages][MR][kStageRow] bytes
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
@@ -232,8 +232,31 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A,
         const int at = (nl / 16) * 256 + (m + 16 * (nl % 16 / 4)) * 4 + nl % 4;
         float s = 0.0f;
         for (int v = 0; v < waves; v++) s += red[v * (RT * 256) + at];
-        store_out(C + (int64_t)m * ldc + n0 + nl, s);
+        store_out(C + (int64_t)m * ldc + n0 + nl, branch(m, n0 + nl, s));
     }
+}
+
+template <int RT, int MR, class OT>
+__global__ __launch_bounds__(512) void k_mx_skinny(const __bf16 *__restrict__ A, int64_t lda,
+                                                   const uint8_t *__restrict__ acodes,
+                                                   const uint8_t *__restrict__ ascales, int M,
+                                                   const uint8_t *__restrict__ wcodes,
+                                                   const uint8_t *__restrict__ wscales, int64_t N, int K, int stages,
+                                                   OT *__restrict__ C, int64_t ldc) {
+    skinny_product<RT, MR>(A, lda, acodes, ascales, M, wcodes, wscales, N, K, stages, C, ldc,
+                           [](int, int64_t, float v) { return v; });
+}
+
+// The same with the adapters' branch (mx_adapters.h).
+template <int RT, int MR, class OT>
+__global__ __launch_bounds__(512) void k_adapter_skinny(const __bf16 *__restrict__ A, int64_t lda,
+                                                        const uint8_t *__restrict__ acodes,
+                                                        const uint8_t *__restrict__ ascales, int M,
+                                                        const uint8_t *__restrict__ wcodes,
+                                                        const uint8_t *__restrict__ wscales, int64_t N, int K, int stages,
+                                                        OT *__restrict__ C, int64_t ldc, Adapters ad) {
+    skinny_product<RT, MR>(A, lda, acodes, ascales, M, wcodes, wscales, N, K, stages, C, ldc,
+                           [&](int m, int64_t n, float v) { return v + adapter_value(ad, m, n, N); });
 }
 
 // -------------------------------------------------------------------------------------------------
@@ -276,20 +299,20 @@ __global__ __launch_bounds__(256) void k_mx_zero(OT *C, int64_t M, int64_t N, in
 // -------------------------------------------------------------------------------------------------
 // launches
 // -------------------------------------------------------------------------------------------------
-template <class T, class OT>
-void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) {
+template <class T, class OT, class Args>
+void launch_tile_t(Args p, int splits, void *partial, hipStream_t stream) {
     p.tiles_m = (int)((p.M + T::BM - 1) / T::BM);
     p.tiles_n = (int)((p.N + T::BN - 1) / T::BN);
     const dim3 grid((unsigned)tile_grid((int64_t)p.tiles_m * p.tiles_n), splits);
     if (splits == 1) {
         p.vec_c = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc * sizeof(OT) % 16 == 0;
-        hipLaunchKernelGGL((k_mx_tile<T, OT, false>), grid, dim3(T::NT), 0, stream, p);
+        hipLaunchKernelGGL((k_mx_tile<T, OT, false, Args>), grid, dim3(T::NT), 0, stream, p);
         return;
     }
     OT *c = reinterpret_cast<OT *>(p.c);
     p.c = partial;
     p.vec_c = p.N % 4 == 0;
-    hipLaunchKernelGGL((k_mx_tile<T, float, true>), grid, dim3(T::NT), 0, stream, p);
+    hipLaunchKernelGGL((k_mx_tile<T, float, true, Args>), grid, dim3(T::NT), 0, stream, p);
     const int64_t n = p.M * p.N;
     const float *planes = reinterpret_cast<const float *>(partial);
     if (p.vec_c && reinterpret_cast<uintptr_t>(c) % (4 * sizeof(OT)) == 0 && p.ldc % 4 == 0)
@@ -300,10 +323,9 @@ void launch_tile_t(MxTileArgs p, int splits, void *partial, hipStream_t stream) 
                            n, (uint32_t)p.N, c, p.ldc);
 }
 
-template <class OT>
-hipError_t launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
-                        int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, hipStream_t stream) {
-    MxTileArgs p{};
+template <class OT, class Args>
+hipError_t launch_tiled(Args p, const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+                        OT *c, int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, hipStream_t stream) {
     p.M = M;
     p.N = w->rows;
     p.K = w->cols;
@@ -339,14 +361,20 @@ hipError_t launch_tiled(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, 
     return hipGetLastError();
 }
 
+// ad: null for the product without adapters.
 template <int RT, int MR, class OT>
 void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
-                     int64_t ldc, int waves, int stages, hipStream_t stream) {
+                     int64_t ldc, int waves, int stages, const Adapters *ad, hipStream_t stream) {
     const unsigned wgs = (unsigned)((w->rows + 16 * RT - 1) / (16 * RT));
     const size_t lds = (size_t)waves * (RT * 1024 + stages * MR * kStageRow);
-    hipLaunchKernelGGL((k_mx_skinny<RT, MR, OT>), dim3(wgs), dim3(64 * waves), lds, stream,
-                       reinterpret_cast<const __bf16 *>(a_bf16), lda, a_q ? a_q->codes : nullptr,
-                       a_q ? a_q->scales : nullptr, (int)M, w->codes, w->scales, w->rows, (int)w->cols, stages, c, ldc);
+    const __bf16 *a = reinterpret_cast<const __bf16 *>(a_bf16);
+    const uint8_t *ac = a_q ? a_q->codes : nullptr, *as = a_q ? a_q->scales : nullptr;
+    if (ad)
+        hipLaunchKernelGGL((k_adapter_skinny<RT, MR, OT>), dim3(wgs), dim3(64 * waves), lds, stream, a, lda, ac, as, (int)M,
+                           w->codes, w->scales, w->rows, (int)w->cols, stages, c, ldc, *ad);
+    else
+        hipLaunchKernelGGL((k_mx_skinny<RT, MR, OT>), dim3(wgs), dim3(64 * waves), lds, stream, a, lda, ac, as, (int)M,
+                           w->codes, w->scales, w->rows, (int)w->cols, stages, c, ldc);
 }
 
 // W row tiles per workgroup and its waves.  Every workgroup reads all of A through L2 (16 rows of bf16 are 3.8
@@ -363,31 +391,33 @@ void launch_skinny_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int
 // two fit in LDS only four times.
 template <int MR, class OT>
 void launch_skinny(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w, OT *c,
-                   int64_t ldc, int num_cus, hipStream_t stream) {
+                   int64_t ldc, int num_cus, const Adapters *ad, hipStream_t stream) {
     const int64_t tiles = (w->rows + 15) / 16, groups = (w->cols + kGroup - 1) / kGroup;
     const int64_t share = (tiles + num_cus - 1) / num_cus;
     int waves = (MR == 0 ? share >= 3 : MR == 16 ? groups <= 8 : share == 3) ? 8 : 4;
     while (waves > 1 && waves / 2 >= groups) waves /= 2;  // no more waves than groups to share out
     const int stages = groups > waves ? 2 : 1;
-    if (share >= 3) launch_skinny_t<3, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, stream);
-    else if (share == 2) launch_skinny_t<2, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, stream);
-    else launch_skinny_t<1, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, stream);
+    if (share >= 3) launch_skinny_t<3, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, ad, stream);
+    else if (share == 2) launch_skinny_t<2, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, ad, stream);
+    else launch_skinny_t<1, MR, OT>(a_bf16, a_q, M, lda, w, c, ldc, waves, stages, ad, stream);
 }
 
 template <class OT>
 hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
-                            OT *c, int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus,
+                            OT *c, int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, const Adapters *ad,
                             hipStream_t stream) {
     if (w->cols == 0) {
         const int64_t blocks = std::min<int64_t>((M * w->rows + 255) / 256, 4096);
         hipLaunchKernelGGL(k_mx_zero<OT>, dim3((unsigned)blocks), dim3(256), 0, stream, c, M, w->rows, ldc);
     } else if (M <= kSkinnyMaxM) {
-        if (a_q) launch_skinny<0>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
-        else if (M <= 4) launch_skinny<4>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
-        else if (M <= 8) launch_skinny<8>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
-        else launch_skinny<16>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, stream);
+        if (a_q) launch_skinny<0>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, ad, stream);
+        else if (M <= 4) launch_skinny<4>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, ad, stream);
+        else if (M <= 8) launch_skinny<8>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, ad, stream);
+        else launch_skinny<16>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, ad, stream);
+    } else if (ad) {
+        return launch_tiled(MxAdapterTileArgs{{}, *ad}, a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     } else {
-        return launch_tiled(a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
+        return launch_tiled(MxTileArgs{}, a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     }
     return hipGetLastError();
 }
@@ -401,12 +431,12 @@ size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus)
 
 hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                           void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,
-                          int num_cus, hipStream_t stream) {
+                          int num_cus, hipStream_t stream, const Adapters *ad) {
     if (c_dtype == NVFP4_F32)
         return launch_mx_gemm_t(a_bf16, a_q, M, lda, w, reinterpret_cast<float *>(c), ldc, workspace, workspace_bytes,
-                                num_cus, stream);
+                                num_cus, ad, stream);
     return launch_mx_gemm_t(a_bf16, a_q, M, lda, w, reinterpret_cast<__bf16 *>(c), ldc, workspace, workspace_bytes,
-                            num_cus, stream);
+                            num_cus, ad, stream);
 }
 
 }  // namespace nvfp4

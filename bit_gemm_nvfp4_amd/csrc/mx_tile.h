@@ -4,6 +4,7 @@
 #pragma once
 
 #include "mx.h"
+#include "mx_adapters.h"
 #include "mx_bounds.h"
 #include "mx_plan.h"
 
@@ -418,10 +419,16 @@ struct MxTileArgs {
     int tiles_m, tiles_n;
     int slice_windows;  // windows of 512 columns per K slice (blockIdx.y)
     int vec_c;          // rows of C (of the partial planes) are 16-byte aligned
+    static constexpr bool kAdapters = false;
 };
 
-template <class T, class OT, bool SPLIT>
-__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(MxTileArgs p) {
+struct MxAdapterTileArgs : MxTileArgs {
+    Adapters ad;
+    static constexpr bool kAdapters = true;
+};
+
+template <class T, class OT, bool SPLIT, class Args>
+__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(Args p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
     int tm, tn;
     if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn)) return;
@@ -483,6 +490,11 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     if constexpr (SPLIT) c += (int64_t)blockIdx.y * p.M * p.N;
     const int64_t ldc = SPLIT ? p.N : p.ldc;
     const int64_t mw = m0 + (wave / T::WN) * T::WTM, nw = n0 + (wave % T::WN) * T::WTN;  // the wave's corner
+    if constexpr (Args::kAdapters) {
+        // Of K slices the first has the branch.  (The question stands here without slices too: without it the largest
+        // tile's main loop and the branch share a block of code, and 88 registers a lane go to memory.)
+        if (blockIdx.y == 0) add_adapters<T::TM, T::TN>(p.ad, acc, mw, p.M, nw, p.N);
+    }
     mx_store_tile<T>(lds, acc, c, ldc, mw, p.M, nw, p.N, n0 + T::BN <= p.N && p.vec_c);
 }
 

@@ -1,6 +1,6 @@
 """MXFP4 (E2M1 codes, one power-of-two E8M0 scale per 32 elements of a row): quantization, expansion,
 the product with MXFP4 weights, the mixture-of-experts layer for a few tokens, and products whose rows pick
-their weights: router, products grouped by expert, the layer for any number of tokens.
+their weights: router, products grouped by expert, the layer for any number of tokens, adapters per request.
 
 A thin ctypes binding over the entry points of ``include/mxfp4.h``; the package re-exports its names.
 """
@@ -21,7 +21,7 @@ MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 64, 512, 16
 GROUP_MAX_ROWS, MAX_GROUPS = 1 << 24, MOE_MAX_EXPERTS
 MX_EXPORTED = ["mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_moe", "mxfp4_workspace_size", "mxfp4_route",
                "mxfp4_group_rows", "mxfp4_grouped_gemm", "mxfp4_combine", "mxfp4_experts",
-               "mxfp4_experts_workspace_size"]
+               "mxfp4_experts_workspace_size", "mxfp4_gemm_adapters", "mxfp4_adapters_workspace_size"]
 
 
 class CMXTensor(ctypes.Structure):
@@ -44,8 +44,11 @@ _SIGNATURES.update({
     "mxfp4_experts": [_P, _I64, _I64, _P, _I32, _I64, _I64, _I32, _I32, _I32, _PX, _PX, _P, _I32, _I64, _P, _P, _P, _SZ,
                       _P],
     "mxfp4_experts_workspace_size": [_I64, _I64, _I32, _I64, _I64, _I32, _I32],
+    "mxfp4_gemm_adapters": [_P, _PX, _I64, _I64, _PX, _P, _I64, _I64, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P],
+    "mxfp4_adapters_workspace_size": [_I64, _I64, _I64, _I64, _I32],
 })
-_RESTYPES["mxfp4_workspace_size"] = _RESTYPES["mxfp4_experts_workspace_size"] = _SZ
+for _name in ("mxfp4_workspace_size", "mxfp4_experts_workspace_size", "mxfp4_adapters_workspace_size"):
+    _RESTYPES[_name] = _SZ
 
 
 @dataclass
@@ -408,3 +411,45 @@ def mx_experts(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_
           out.data_ptr(), dt, ld_y, _opt(ids, dev, "ids"), _opt(weights, dev, "weights"), _opt(workspace, dev, "workspace"),
           _nbytes(workspace))
     return (out, ids, weights) if routing else out
+
+
+def mx_adapters_workspace(m: int, w: MXFP4Tensor, rank: int, quantized_acts: bool = False) -> torch.Tensor | None:
+    """A workspace for mx_gemm_adapters with m rows (None without any).  Its contents do not matter; calls that share one
+    must be ordered (same stream, or events)."""
+    dev = w.codes.device
+    args = (m, w.shape[0], w.shape[1], rank, 1 if quantized_acts else 0)
+    if dev.index == _current_device():  # the size is planned for the current device
+        return _workspace(int(load_library().mxfp4_adapters_workspace_size(*args)), dev)
+    with torch.cuda.device(dev.index):
+        return _workspace(int(load_library().mxfp4_adapters_workspace_size(*args)), dev)
+
+
+def mx_gemm_adapters(a: torch.Tensor, w: MXFP4Tensor, down: torch.Tensor, up: torch.Tensor, index: torch.Tensor,
+                     scales: torch.Tensor | None = None, a_q: MXFP4Tensor | None = None, dtype: torch.dtype = torch.float32,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A projection that requests share, with low-rank adapters of their own: C[m] = A[m] . W^T + scales[i] (A[m] .
+    down[i]^T) . up[i]^T with i = index[m] (int32 [M], any order; outside 0 .. adapters - 1: no adapter).
+
+    a: bf16 [M, K]; a_q: its MXFP4 form, for a W4A4 product (the branch takes `a`); w [N, K]; down [adapters, rank, K] and up
+    [adapters, N, rank] bf16, dense, rank a multiple of 8 up to 256; scales fp32 [adapters].  C fp32 or bf16, rounded once."""
+    assert isinstance(w, MXFP4Tensor), "w: an MXFP4Tensor is required"
+    n, k = w.shape
+    dev = w.codes.device
+    assert a.dtype is torch.bfloat16 and a.device == dev, f"a: a bf16 tensor on {dev} is required"
+    lda, m = _rows(a, "a", k), a.shape[0]
+    assert down.dim() == 3, f"down: [adapters, rank, K] is required, not {tuple(down.shape)}"
+    count, rank = down.shape[0], down.shape[1]
+    a_ct = None
+    if a_q is not None:
+        assert a_q.shape == (m, k) and a_q.codes.device == dev, f"a_q: {a_q.shape} on {a_q.codes.device}, expected {(m, k)} on {dev}"
+        a_ct = ctypes.byref(a_q.c())
+    down_ptr = _words(down, "down", dev, torch.bfloat16, count, rank, k)
+    up_ptr = _words(up, "up", dev, torch.bfloat16, count, n, rank)
+    index_ptr = _words(index, "index", dev, torch.int32, m)
+    scales_ptr = None if scales is None else _words(scales, "scales", dev, torch.float32, count)
+    out, ldc, dt = _out(out, m, n, dtype, dev, "out")
+    if workspace is None:
+        workspace = mx_adapters_workspace(m, w, rank, a_q is not None)
+    _call("mxfp4_gemm_adapters", dev, a.data_ptr(), a_ct, m, lda, ctypes.byref(w.c()), index_ptr, count, rank, down_ptr, up_ptr,
+          scales_ptr, out.data_ptr(), dt, ldc, _opt(workspace, dev, "workspace"), _nbytes(workspace))
+    return out

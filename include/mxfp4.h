@@ -206,6 +206,33 @@ nvfp4_status mxfp4_experts(const void *x, int64_t tokens, int64_t ld_x, const vo
 size_t mxfp4_experts_workspace_size(int64_t tokens, int64_t experts, int top_k, int64_t H, int64_t I, int quantize_acts,
                                     nvfp4_dtype y_dtype);
 
+/* Largest arguments of mxfp4_gemm_adapters. */
+enum { MXFP4_MAX_ADAPTERS = 1 << 16, MXFP4_MAX_RANK = 256 };
+
+/*
+ * mxfp4_gemm_adapters -- a projection that requests share, with low-rank adapters that are their own:
+ *   C[m] = A[m] . W^T + s[i] (A[m] . V[i]^T) . U[i]^T,   i = index[m]
+ *   a_bf16  [M x K] bf16, row stride lda: the activations of the branch, and of the product when a_q is NULL (W4A16)
+ *   a_q     NULL, or the MXFP4 activations [M x K] of a W4A4 product
+ *   w       [N x K] MXFP4
+ *   index   [M]: the adapter of each row, in any order; outside 0 .. adapters - 1: none (the row is the product's)
+ *   down    V [adapters x rank x K] bf16, up U [adapters x N x rank] bf16, dense; rank 8 .. MXFP4_MAX_RANK, a multiple of 8
+ *           (an adapter of a lower rank is filled up with zeros)
+ *   scales  [adapters] fp32, or NULL for 1
+ *   c       [M x N] fp32 or bf16 (row stride ldc)
+ * Sums are fp32 (A . V^T too, which passes on with fp32's 24 bits), and C is rounded once.  What an adapter holds reaches
+ * the rows that name it and no others.  A NaN or infinity in V or U gives NaN or infinity in rows that name that adapter.
+ * index, down, up and scales are read on the device.
+ * workspace (16-byte aligned): at least M * rank * 4 bytes, rounded up to 256 (NVFP4_ERR_WORKSPACE for less; none without
+ * adapters); with mxfp4_adapters_workspace_size(...) bytes a long K may be split as in mxfp4_gemm.  quantized_acts: whether
+ * a_q is given.  M <= MXFP4_GROUP_MAX_ROWS; else limits and errors as for mxfp4_gemm.
+ */
+nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+                                 const int32_t *index, int64_t adapters, int64_t rank, const void *down, const void *up,
+                                 const float *scales, void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+size_t mxfp4_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int quantized_acts);
+
 /* Workspace bytes of an entry point (0 when none); see the selectors for the arguments.  Planned for
  * the current device (an MI355X's 256 CUs when none can be queried). */
 size_t mxfp4_workspace_size(int op, int64_t m, int64_t n, int64_t k);

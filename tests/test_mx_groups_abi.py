@@ -152,3 +152,28 @@ def test_binding_refusals(nv):
         nv.mx_group_rows(t, 4)
     with pytest.raises(AssertionError):
         nv.mx_grouped_gemm(torch.zeros((4, 64)), t, t)
+
+
+def test_adapters_refusals(nv):
+    size = nv.lib.mxfp4_adapters_workspace_size
+    M, N, K, R, C = 100, 64, 128, 16, 3
+    ws = size(M, N, K, R, 0)
+    assert ws >= M * R * 4 and size(0, N, K, R, 0) == 0 and size(M, N, K, 12, 0) == 0 and size(MAX_ROWS + 1, N, K, R, 0) == 0
+
+    def call(a16=P(FAKE), aq=None, m=M, lda=K, wt=_mx(N, K), idx=P(FAKE), cnt=C, r=R, dn=P(FAKE), up=P(FAKE), sc=None, c=P(FAKE), dt=0,
+             ldc=N, w=P(FAKE), wsb=ws):
+        return nv.lib.mxfp4_gemm_adapters(a16, _ref(aq), m, lda, _ref(wt), idx, cnt, r, dn, up, sc, c, dt, ldc, w, wsb, None)
+    assert call(wt=None) == 1 and call(a16=None) == 1 and call(a16=None, aq=_mx(M, K)) == 1   # the branch takes bf16
+    assert call(idx=None) == 1 and call(dn=None) == 1 and call(up=None) == 1 and call(c=None) == 1
+    assert call(dt=2) == 4
+    assert call(m=-1) == 2 and call(m=MAX_ROWS + 1) == 2 and call(lda=96) == 2 and call(ldc=63) == 2 and call(cnt=-1) == 2
+    assert call(cnt=(1 << 16) + 1) == 2 and call(lda=(1 << 22) + 8) == 2
+    for rank in (0, 4, 12, 264):
+        assert call(r=rank) == 2
+    assert call(aq=_mx(M - 1, K)) == 2 and call(aq=_mx(M, K + 32)) == 2
+    assert call(lda=132) == 3 and call(dn=P(FAKE + 8)) == 3 and call(up=P(FAKE + 8)) == 3 and call(idx=P(FAKE + 2)) == 3
+    assert call(sc=P(FAKE + 2)) == 3 and call(c=P(FAKE + 2)) == 3 and call(w=P(FAKE + 8)) == 3
+    need = (M * R * 4 + 255) // 256 * 256
+    assert call(w=None) == 5 and call(wsb=need - 1) == 5
+    if not _gpu():
+        assert call() == 7 and call(wsb=need) == 7 and call(cnt=0, dn=None, up=None, w=None) == 7 and call(aq=_mx(M, K)) == 7
