@@ -176,8 +176,8 @@ hipError_t launch_mx_quantize(const void *x, nvfp4_dtype dt, int64_t ld_x, const
 hipError_t launch_mx_dequantize(const mxfp4_tensor *in, void *out, nvfp4_dtype out_dtype, int64_t ld_out,
                                 hipStream_t stream);
 
-// Workspace of mxfp4_gemm: the partial sums of the planned K slices, 0 when unsplit.
-size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus);
+// Workspace of mxfp4_gemm: the partial sums of the planned K slices, 0 when unsplit.  first_shape: of the tile shapes.
+size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus, int first_shape = 0);
 hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                           void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace, size_t workspace_bytes,
                           int num_cus, hipStream_t stream, const struct Adapters *ad = nullptr);
@@ -213,8 +213,9 @@ struct MxRouteArgs {
 size_t mx_route_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts);
 hipError_t launch_mx_route(const MxRouteArgs &a, void *workspace, hipStream_t stream);
 size_t mx_sort_ws_bytes(int64_t pairs, int64_t groups);
+// rest: ids outside 0 .. groups - 2 belong to the last group instead of none.
 hipError_t launch_mx_sort(const int32_t *ids, int64_t rows, int per_row, int64_t groups, int32_t *offsets, int32_t *out_rows,
-                          int32_t *places, void *workspace, hipStream_t stream);
+                          int32_t *places, bool rest, void *workspace, hipStream_t stream);
 hipError_t launch_mx_combine(const void *z, nvfp4_dtype z_dtype, int64_t z_rows, int64_t ld_z, const int32_t *places,
                              const float *weights, int64_t tokens, int top_k, int64_t cols, void *y, nvfp4_dtype y_dtype,
                              int64_t ld_y, hipStream_t stream);

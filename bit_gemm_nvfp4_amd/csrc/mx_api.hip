@@ -6,8 +6,10 @@
 #include "internal.h"
 #include "mx.h"
 #include "mx_adapters.h"
+#include "mx_plan.h"
 #include "mxfp4.h"
 
+#include <algorithm>
 #include <initializer_list>
 
 using namespace nvfp4;
@@ -71,8 +73,24 @@ nvfp4_status first_of(std::initializer_list<nvfp4_status> all) {
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-// T at the front of the workspace of mxfp4_gemm_adapters.
-size_t adapters_t_bytes(int64_t M, int64_t rank) { return align256((size_t)M * rank * 4); }
+// The workspace of mxfp4_gemm_adapters: T (fp32, or three bf16 planes); the branch's sums where it has them; where the rows
+// are sorted by adapter their order, the groups' offsets and the sort's own workspace; then the product's.
+struct AdaptersWs {
+    size_t sums, order, offsets, sort, product;
+    bool few, sorted, summed;
+};
+AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t rank, int64_t adapters) {
+    AdaptersWs w{};
+    w.few = M <= kAdapterElementRows;
+    w.summed = w.few && M > 16;  // (with fewer the product forms them)
+    w.sorted = !w.few && adapters > 1 && adapters < MXFP4_MAX_GROUPS;
+    w.sums = align256((size_t)M * rank * (w.few ? 4 : 2 * kAdapterPlanes));
+    w.order = w.sums + (w.summed ? align256((size_t)M * N * 4) : 0);
+    w.offsets = w.order + (w.sorted ? align256((size_t)M * 4) : 0);
+    w.sort = w.offsets + (w.sorted ? align256((size_t)(adapters + 2) * 4) : 0);
+    w.product = w.sort + (w.sorted ? align256(mx_sort_ws_bytes(M, adapters + 1)) : 0);
+    return w;
+}
 
 bool rank_fits(int64_t rank) { return rank >= 8 && rank <= MXFP4_MAX_RANK && rank % 8 == 0; }
 
@@ -253,7 +271,7 @@ nvfp4_status mxfp4_group_rows(const int32_t *ids, int64_t tokens, int per_token,
     if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
     if (mx_sort_ws_bytes(tokens * per_token, groups) > (workspace ? workspace_bytes : 0)) return NVFP4_ERR_WORKSPACE;
     if (current_device_cus() == 0) return NVFP4_ERR_DEVICE;
-    return launched(launch_mx_sort(ids, tokens, per_token, groups, offsets, rows, places, workspace, stream));
+    return launched(launch_mx_sort(ids, tokens, per_token, groups, offsets, rows, places, false, workspace, stream));
 }
 
 nvfp4_status mxfp4_grouped_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t a_rows, int64_t lda, const int32_t *map,
@@ -400,10 +418,14 @@ nvfp4_status mxfp4_experts(const void *x, int64_t tokens, int64_t ld_x, const vo
     return launched(launch_mx_combine(ws + at.z, y_dtype, pairs, H, words(at.places), wts, tokens, top_k, H, y, y_dtype, ld_y, stream));
 }
 
-size_t mxfp4_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int quantized_acts) {
-    if (M <= 0 || M > MXFP4_GROUP_MAX_ROWS || N <= 0 || N > kMaxDim || K <= 0 || K > kMaxDim || !rank_fits(rank)) return 0;
+size_t mxfp4_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank, int quantized_acts) {
+    if (M <= 0 || M > MXFP4_GROUP_MAX_ROWS || N <= 0 || N > kMaxDim || K <= 0 || K > kMaxDim || adapters < 0 ||
+        adapters > MXFP4_MAX_ADAPTERS || !rank_fits(rank))
+        return 0;
     const int cus = current_device_cus();
-    return adapters_t_bytes(M, rank) + mx_gemm_ws_bytes(M, N, K, quantized_acts != 0, cus > 0 ? cus : 256);
+    const AdaptersWs at = adapters_ws(M, N, rank, adapters);
+    return (adapters > 0 ? at.product : 0) + mx_gemm_ws_bytes(M, N, K, quantized_acts != 0, cus > 0 ? cus : 256,
+                                                              adapters > 0 && at.summed ? kFirstLowShape : 0);
 }
 
 nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
@@ -419,7 +441,7 @@ nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, in
         return NVFP4_ERR_SHAPE;
     st = check_rows(a_bf16, M, K, lda, 2, 16);
     if (st != NVFP4_OK) return st;
-    if (M > 16 && lda > kMaxTileLd) return NVFP4_ERR_SHAPE;
+    if (lda > kMaxTileLd) return NVFP4_ERR_SHAPE;
     if (a_q) {
         st = check_mx(a_q);
         if (st != NVFP4_OK) return st;
@@ -430,22 +452,30 @@ nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, in
                    check_rows(c, M, N, ldc, eb, eb), check_words(index, M > 0), check_words(scales, false)});
     if (st != NVFP4_OK) return st;
     if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
-    const size_t t_bytes = adapters_t_bytes(M, rank), have = workspace ? workspace_bytes : 0;
+    const size_t have = workspace ? workspace_bytes : 0;
     const bool branch = M > 0 && N > 0 && K > 0 && adapters > 0;
-    if (branch && have < t_bytes) return NVFP4_ERR_WORKSPACE;
+    const AdaptersWs at = adapters_ws(M, N, rank, adapters);
+    if (branch && have < at.product) return NVFP4_ERR_WORKSPACE;
     const int cus = current_device_cus();
     if (cus == 0) return NVFP4_ERR_DEVICE;
     if (M == 0 || N == 0) return NVFP4_OK;
-    const Adapters ad{reinterpret_cast<const float *>(workspace), reinterpret_cast<const __bf16 *>(up), index, (int)adapters,
-                      (int)rank};
-    if (branch) {
-        const AdapterDownArgs d{a_bf16, M, lda, K, down, scales, index, (int)adapters, (int)rank, reinterpret_cast<float *>(workspace)};
-        const hipError_t e = launch_adapter_down(d, cus, stream);
-        if (e != hipSuccess) return launched(e);
-    }
-    uint8_t *planes = have > t_bytes ? reinterpret_cast<uint8_t *>(workspace) + t_bytes : nullptr;
-    return launched(launch_mx_gemm(a_q ? nullptr : a_bf16, a_q, M, lda, w, c, c_dtype, ldc, planes, planes ? have - t_bytes : 0,
-                                   cus, stream, branch ? &ad : nullptr));
+    uint8_t *const ws = reinterpret_cast<uint8_t *>(workspace);
+    if (!branch) return launched(launch_mx_gemm(a_q ? nullptr : a_bf16, a_q, M, lda, w, c, c_dtype, ldc, ws, have, cus, stream));
+    float *const t = at.few ? reinterpret_cast<float *>(ws) : nullptr, *const sums = at.summed ? reinterpret_cast<float *>(ws + at.sums) : nullptr;
+    __bf16 *const t_planes = t ? nullptr : reinterpret_cast<__bf16 *>(ws);
+    // rows in another order are picked from one buffer of all of A
+    int32_t *const order = at.sorted && M * std::max(lda * 2, K) < ((int64_t)1 << 31) ? reinterpret_cast<int32_t *>(ws + at.order) : nullptr;
+    hipError_t e = hipSuccess;
+    if (order)
+        e = launch_mx_sort(index, M, 1, adapters + 1, reinterpret_cast<int32_t *>(ws + at.offsets), order, nullptr, true, ws + at.sort, stream);
+    if (e != hipSuccess) return launched(e);
+    e = launch_adapter_down(AdapterDownArgs{a_bf16, M, lda, K, down, scales, index, order, (int)adapters, (int)rank, t, t_planes}, cus, stream);
+    if (e != hipSuccess) return launched(e);
+    const Adapters ad{t, t_planes, sums, reinterpret_cast<const __bf16 *>(up), index, order, (int)adapters, (int)rank};
+    if (sums) e = launch_adapter_sums(ad, M, N, sums, stream);
+    if (e != hipSuccess) return launched(e);
+    return launched(launch_mx_gemm(a_q ? nullptr : a_bf16, a_q, M, lda, w, c, c_dtype, ldc, ws + at.product, have - at.product, cus,
+                                   stream, &ad));
 }
 
 }  // extern "C"

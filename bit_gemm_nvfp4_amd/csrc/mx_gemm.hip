@@ -22,13 +22,17 @@
 
 #include "internal.h"
 #include "mx.h"
-#include "mx_tile.h"
+#include "mx_adapters.h"
 
 namespace nvfp4 {
 
 namespace {
 
 constexpr int kSkinnyMaxM = 16;
+static_assert(kTileCost[0][kFirstLowShape].bm <= kAdapterElementRows && kTileCost[1][kFirstLowShape].bm <= kAdapterElementRows &&
+                  kTileCost[0][4].bm <= kAdapterElementRows && kTileCost[1][4].bm <= kAdapterElementRows && kTileShapes == 5,
+              "tiles that take the branch's sums");
+static_assert(kSkinnyMaxM <= kAdapterElementRows, "the form of T that the products of few rows take");
 // -------------------------------------------------------------------------------------------------
 // M <= 16
 // -------------------------------------------------------------------------------------------------
@@ -299,6 +303,15 @@ __global__ __launch_bounds__(256) void k_mx_zero(OT *C, int64_t M, int64_t N, in
 // -------------------------------------------------------------------------------------------------
 // launches
 // -------------------------------------------------------------------------------------------------
+template <class T, class OT, bool SPLIT>
+void launch_tile_kernel(const MxTileArgs &p, dim3 grid, hipStream_t stream) {
+    hipLaunchKernelGGL((k_mx_tile<T, OT, SPLIT>), grid, dim3(T::NT), 0, stream, p);
+}
+template <class T, class OT, bool SPLIT>
+void launch_tile_kernel(const MxAdapterTileArgs &p, dim3 grid, hipStream_t stream) {
+    hipLaunchKernelGGL((k_adapter_tile<T, OT, SPLIT>), grid, dim3(T::NT), 0, stream, p);
+}
+
 template <class T, class OT, class Args>
 void launch_tile_t(Args p, int splits, void *partial, hipStream_t stream) {
     p.tiles_m = (int)((p.M + T::BM - 1) / T::BM);
@@ -306,13 +319,13 @@ void launch_tile_t(Args p, int splits, void *partial, hipStream_t stream) {
     const dim3 grid((unsigned)tile_grid((int64_t)p.tiles_m * p.tiles_n), splits);
     if (splits == 1) {
         p.vec_c = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc * sizeof(OT) % 16 == 0;
-        hipLaunchKernelGGL((k_mx_tile<T, OT, false, Args>), grid, dim3(T::NT), 0, stream, p);
+        launch_tile_kernel<T, OT, false>(p, grid, stream);
         return;
     }
     OT *c = reinterpret_cast<OT *>(p.c);
     p.c = partial;
     p.vec_c = p.N % 4 == 0;
-    hipLaunchKernelGGL((k_mx_tile<T, float, true, Args>), grid, dim3(T::NT), 0, stream, p);
+    launch_tile_kernel<T, float, true>(p, grid, stream);
     const int64_t n = p.M * p.N;
     const float *planes = reinterpret_cast<const float *>(partial);
     if (p.vec_c && reinterpret_cast<uintptr_t>(c) % (4 * sizeof(OT)) == 0 && p.ldc % 4 == 0)
@@ -324,7 +337,7 @@ void launch_tile_t(Args p, int splits, void *partial, hipStream_t stream) {
 }
 
 template <class OT, class Args>
-hipError_t launch_tiled(Args p, const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
+hipError_t launch_tiled(Args p, int first_shape, const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                         OT *c, int64_t ldc, void *workspace, size_t workspace_bytes, int num_cus, hipStream_t stream) {
     p.M = M;
     p.N = w->rows;
@@ -338,7 +351,7 @@ hipError_t launch_tiled(Args p, const void *a_bf16, const mxfp4_tensor *a_q, int
     p.ascales = a_mx ? a_q->scales : nullptr;
     p.a_row_bytes = a_mx ? p.K / 2 : lda * 2;
     p.a_row_len = a_mx ? p.K / 2 : p.K * 2;
-    const MxPlan plan = plan_mx_within(M, p.N, p.K, a_mx, num_cus, workspace ? workspace_bytes : 0);
+    const MxPlan plan = plan_mx_within(M, p.N, p.K, a_mx, num_cus, workspace ? workspace_bytes : 0, first_shape);
     if (plan.cfg < 0) return hipErrorInvalidConfiguration;
     p.slice_windows = plan.slice_windows;
     if (a_mx) {
@@ -415,18 +428,18 @@ hipError_t launch_mx_gemm_t(const void *a_bf16, const mxfp4_tensor *a_q, int64_t
         else if (M <= 8) launch_skinny<8>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, ad, stream);
         else launch_skinny<16>(a_bf16, a_q, M, lda, w, c, ldc, num_cus, ad, stream);
     } else if (ad) {
-        return launch_tiled(MxAdapterTileArgs{{}, *ad}, a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
+        return launch_tiled(MxAdapterTileArgs{{}, *ad}, ad->sums ? kFirstLowShape : 0, a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     } else {
-        return launch_tiled(MxTileArgs{}, a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
+        return launch_tiled(MxTileArgs{}, 0, a_bf16, a_q, M, lda, w, c, ldc, workspace, workspace_bytes, num_cus, stream);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus) {
+size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_mx, int num_cus, int first_shape) {
     if (M <= kSkinnyMaxM || N <= 0 || K <= 0) return 0;
-    return plan_ws_bytes(plan_mx(M, N, K, a_mx, num_cus), M, N);
+    return plan_ws_bytes(plan_mx(M, N, K, a_mx, num_cus, kMaxSplits, first_shape), M, N);
 }
 
 hipError_t launch_mx_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,

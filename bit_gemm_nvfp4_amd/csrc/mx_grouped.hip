@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_swiglu(uint8_t *lds, const f32x16 (&acc)[T
 template <class T, class OT, bool SWIGLU>
 __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GroupedDev p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the tile, its group and its rows
     int tiles_m = 0;
     TileScan sc{};
@@ -138,8 +138,7 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
 
     constexpr int COLS = SWIGLU ? T::BN / 2 : T::BN;  // columns of C
     const int n0 = tn * COLS;
-    const int K = p.K, kb = K / kMxBlock, wrb = K / 2;
-    const int arb = (int)p.a_row_bytes, alen = (int)p.a_row_len;
+    const int K = p.K;
     // rows of A and W of a tile row, or -1
     auto a_row = [&](int r) -> int {
         if (r >= mrows) return -1;
@@ -155,57 +154,27 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
             return n0 + r < p.cols ? r : -1;
         }
     };
-    const uint8_t *abase = p.map ? p.a : p.a + (int64_t)lo * arb;
-    const int64_t asc = p.map ? 0 : lo, w0 = (int64_t)g * p.N + n0;
-    const uint32_t abytes = p.map && p.a_rows == 0 ? 0u : (uint32_t)((p.map ? p.a_rows - 1 : mrows - 1) * (int64_t)arb + alen);
-    const uint32_t wbytes = (uint32_t)(((SWIGLU ? p.cols : 0) + min(COLS, p.cols - n0)) * (int64_t)wrb);
-    const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(abase, abytes), rw = uniform_rsrc(p.wcodes + w0 * wrb, wbytes);
-
-    // Direct-to-LDS loads: unit u = wave + NW i fills 1 KiB of a stage (8 rows of 128 bytes, or 32 of 32).  Every
-    // lane's offset is its own row's; those without a row, and pieces past the end of a row, lie past the buffers'
-    // ranges and load zeros.
-    constexpr int A_PER = T::A_UNITS / T::NW, RPU = 64 / T::W_PIECES;
-    const int ar = wave * 8 + lane / 8, wr = wave * RPU + lane / T::W_PIECES;
-    const int apb = swizzle<8>(ar, lane % 8) * 16, wpb = swizzle<T::W_PIECES>(wr, lane % T::W_PIECES) * 16;
-    uint32_t off[T::UPW];
-#pragma unroll
-    for (int i = 0; i < T::UPW; i++) {
-        const int r = i < A_PER ? a_row(i * (T::NW * 8) + ar) : w_row((i - A_PER) * (T::NW * RPU) + wr);
-        off[i] = bounds::row_off(r, i < A_PER ? arb : wrb, i < A_PER ? apb : wpb);
-    }
-    auto load_stage = [&](int s) {
-        uint8_t *dst = lds + (s % T::NST) * T::STAGE + wave * 1024;
-        const int ao = s * T::A_ROWB, wo = s * T::W_ROWB;
-        const uint32_t as = bounds::part_soff(ao, abytes), ws = bounds::part_soff(wo, wbytes);
-#pragma unroll
-        for (int i = 0; i < T::UPW; i++)
-            load_to_lds16(i < A_PER ? ra : rw, dst + i * (T::NW * 1024),
-                          i < A_PER ? bounds::step_off(off[i], ao, apb, alen) : bounds::step_off(off[i], wo, wpb, wrb),
-                          i < A_PER ? as : ws);
-    };
-    const uint8_t *srow[T::SC_PER];
-#pragma unroll
-    for (int i = 0; i < T::SC_PER; i++) {
-        const int r = tid + i * T::NT;
-        srow[i] = nullptr;
-        if (r < T::SA_ROWS) {
-            const int s = a_row(r);
-            if (s >= 0) srow[i] = p.ascales + (asc + s) * kb;
-        } else if (r < T::SC_ROWS) {
-            const int s = w_row(r - T::SA_ROWS);
-            if (s >= 0) srow[i] = p.wscales + (w0 + s) * kb;
-        }
-    }
+    const int64_t arow0 = p.map ? 0 : lo, wrow0 = (int64_t)g * p.N + n0;
+    const int64_t arows = p.map ? p.a_rows : mrows, wrows = (SWIGLU ? p.cols : 0) + min(COLS, p.cols - n0);
+    const MxPicked picked{p.a + arow0 * p.a_row_bytes,
+                          p.ascales + arow0 * (K / kMxBlock),
+                          arows ? (uint32_t)((arows - 1) * p.a_row_bytes + p.a_row_len) : 0u,
+                          (int)p.a_row_bytes,
+                          (int)p.a_row_len,
+                          p.wcodes + wrow0 * (K / 2),
+                          p.wscales + wrow0 * (K / kMxBlock),
+                          (uint32_t)(wrows * (K / 2)),
+                          K};
     f32x16 acc[T::TM][T::TN] = {};
-    const int windows = (K + kGroup - 1) / kGroup;
-    mx_tile_product<T>(lds, kb, 0, windows, (K + T::BK - 1) / T::BK, srow, load_stage, acc);
+    mx_picked_product<T>(lds, picked, 0, (K + kGroup - 1) / kGroup, a_row, w_row, acc);
 
     const int mw = wave / T::WN * T::WTM;
     if constexpr (SWIGLU) {
         store_swiglu<T, OT>(lds, acc, p, lo, mw, mrows, n0 + wave % T::WN * 32);
     } else {
         OT *c = reinterpret_cast<OT *>(p.c) + (int64_t)lo * p.ldc;
-        mx_store_tile<T>(lds, acc, c, p.ldc, mw, mrows, n0 + wave % T::WN * T::WTN, p.cols, n0 + T::BN <= p.cols && p.vec_c);
+        mx_store_tile<T>(lds, acc, c, p.ldc, mw, mrows, n0 + wave % T::WN * T::WTN, p.cols, n0 + T::BN <= p.cols && p.vec_c,
+                         [](int64_t m, int, int) { return m; });
     }
 }
 
@@ -226,14 +195,13 @@ hipError_t launch_cfg(const GroupedDev &p, int cfg, hipStream_t stream) {
         case 0: return launch_t<MxTile<256, 256, 2, 4, true, 2>, OT, SWIGLU>(p, stream);
         case 1: return launch_t<MxTile<128, 256, 2, 4, true, 3>, OT, SWIGLU>(p, stream);
         case 2: return launch_t<MxTile<128, 128, 4, 2, true, 3>, OT, SWIGLU>(p, stream);
-        case 3: return launch_t<MxTile<64, 128, 2, 2, true, 3>, OT, SWIGLU>(p, stream);
-        default: return launch_t<MxTile<32, 128, 1, 2, true, 3>, OT, SWIGLU>(p, stream);
+        default: return launch_t<MxTile<64, 128, 2, 2, true, 3>, OT, SWIGLU>(p, stream);
         }
     } else {
         switch (cfg) {
-        case 0: return launch_t<MxTile<256, 256, 2, 4, false, 3>, OT, SWIGLU>(p, stream);
-        case 1: return launch_t<MxTile<128, 256, 2, 4, false, 3>, OT, SWIGLU>(p, stream);
-        case 2: return launch_t<MxTile<128, 128, 2, 2, false, 3>, OT, SWIGLU>(p, stream);
+        case 0: return launch_t<MxTile<128, 256, 1, 4, false, 3>, OT, SWIGLU>(p, stream);
+        case 1: return launch_t<MxTile<64, 256, 1, 4, false, 3>, OT, SWIGLU>(p, stream);
+        case 2: return launch_t<MxTile<32, 256, 1, 4, false, 4>, OT, SWIGLU>(p, stream);
         case 3: return launch_t<MxTile<64, 128, 2, 2, false, 4>, OT, SWIGLU>(p, stream);
         default: return launch_t<MxTile<32, 128, 1, 2, false, 4>, OT, SWIGLU>(p, stream);
         }

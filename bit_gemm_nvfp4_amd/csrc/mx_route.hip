@@ -38,6 +38,7 @@ struct RouteDev {
     int32_t *offsets, *rows, *places;
     int32_t *hist;  // [blocks][E]
     int blocks;
+    bool rest;    // choices outside the groups belong to the last one
     int64_t run;  // pairs per workgroup; whole rows for k_mx_route
 };
 
@@ -72,19 +73,43 @@ __device__ __forceinline__ void wave_part(int64_t n, int wave, int64_t &lo, int6
     hi = min(n, lo + q);
 }
 
-// Counts per wave and group of the workgroup's pairs n0 .. n0 + n - 1.  Lanes of one group let the first of them add.
-__device__ __forceinline__ void count_pairs(const RouteDev &a, SortShared &s, int64_t n0, int64_t n, int bits) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int j = tid; j < kWaves * a.E; j += kThreads) s.cnt[j / a.E][j % a.E] = 0;
-    __syncthreads();
+// The group of pair i, outside 0 .. E - 1 where it has none.
+__device__ __forceinline__ int group_of(const RouteDev &a, int64_t i) {
+    const int g = a.ids[i];
+    return a.rest && (unsigned)g >= (unsigned)a.E - 1 ? a.E - 1 : g;
+}
+
+__device__ __forceinline__ void clear_counts(const RouteDev &a, SortShared &s, int lane, int wave) {
+    for (int e = lane; e < a.E; e += 64) s.cnt[wave][e] = 0;  // a wave's own line
+}
+
+// The wave's pairs a block of kAhead x 64 at a time, their groups loaded side by side: each(place of the lane's pair, or -1
+// behind the last; its group).  (One at a time, the two passes over 4096 pairs in one workgroup waited eight times.)
+constexpr int kAhead = 4;
+template <class Each>
+__device__ __forceinline__ void each_pair(const RouteDev &a, int64_t n0, int64_t n, Each each) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int64_t lo, hi;
     wave_part(n, wave, lo, hi);
-    for (int64_t i = lo; i < hi; i += 64) {
-        const int g = i + lane < hi ? a.ids[n0 + i + lane] : -1;
+    for (int64_t i = lo; i < hi; i += 64 * kAhead) {
+        int g[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; q++) g[q] = i + 64 * q + lane < hi ? group_of(a, n0 + i + 64 * q + lane) : -1;
+#pragma unroll
+        for (int q = 0; q < kAhead; q++)
+            if (i + 64 * q < hi) each(i + 64 * q + lane < hi ? n0 + i + 64 * q + lane : -1, g[q]);
+    }
+}
+
+// Counts per wave and group of the workgroup's pairs n0 .. n0 + n - 1.  Lanes of one group let the first of them add.
+__device__ __forceinline__ void count_pairs(const RouteDev &a, SortShared &s, int64_t n0, int64_t n, int bits) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    clear_counts(a, s, lane, wave);
+    each_pair(a, n0, n, [&](int64_t, int g) {
         const bool ok = (unsigned)g < (unsigned)a.E;
         const uint64_t m = same_group(g, ok, bits);
         if (ok && lane == __builtin_ctzll(m)) s.cnt[wave][g] += __popcll(m);
-    }
+    });
     __syncthreads();
 }
 
@@ -97,11 +122,19 @@ __device__ void place_pairs(const RouteDev &a, SortShared &s, int block, int64_t
     const int parts = kThreads / width, e = tid & (width - 1), part = tid / width;
     uint32_t total = 0, before = 0;
     if (a.blocks > 1 && e < a.E) {
-        const int per = (a.blocks + parts - 1) / parts, b1 = min(a.blocks, (part + 1) * per);
-        for (int b = part * per; b < b1; b++) {
-            const uint32_t v = (uint32_t)a.hist[(int64_t)b * a.E + e];
-            total += v;
-            before += b < block ? v : 0;
+        // rows part, part + parts, ... of the table, eight loads side by side
+        for (int b0 = part; b0 < a.blocks; b0 += 8 * parts) {
+            uint32_t v[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const int b = b0 + q * parts;
+                v[q] = b < a.blocks ? (uint32_t)a.hist[(int64_t)b * a.E + e] : 0;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                total += v[q];
+                before += b0 + q * parts < block ? v[q] : 0;
+            }
         }
     } else if (a.blocks == 1 && part == 0 && e < a.E) {
         total = group_count(s, e);
@@ -142,11 +175,7 @@ __device__ void place_pairs(const RouteDev &a, SortShared &s, int block, int64_t
     }
     if (block == 0 && tid == 0) a.offsets[a.E] = (int32_t)all;
     __syncthreads();
-    int64_t lo, hi;
-    wave_part(n, wave, lo, hi);
-    for (int64_t i = lo; i < hi; i += 64) {
-        const bool in = i + lane < hi;
-        const int g = in ? a.ids[n0 + i + lane] : -1;
+    each_pair(a, n0, n, [&](int64_t i, int g) {
         const bool ok = (unsigned)g < (unsigned)a.E;
         const uint64_t m = same_group(g, ok, bits);
         int at = -1;
@@ -154,10 +183,10 @@ __device__ void place_pairs(const RouteDev &a, SortShared &s, int block, int64_t
             const uint32_t base = s.cnt[wave][g];
             at = (int)(base + __popcll(m & ((1ull << lane) - 1)));
             if (lane == __builtin_ctzll(m)) s.cnt[wave][g] = base + __popcll(m);
-            a.rows[at] = (int32_t)((uint32_t)(n0 + i + lane) / (uint32_t)a.k);
+            a.rows[at] = a.k == 1 ? (int32_t)i : (int32_t)((uint32_t)i / (uint32_t)a.k);
         }
-        if (in && a.places) a.places[n0 + i + lane] = at;
-    }
+        if (i >= 0 && a.places) a.places[i] = at;
+    });
     // positions behind the last group
     for (int64_t i = all + (int64_t)block * kThreads + tid; i < a.P; i += (int64_t)a.blocks * kThreads) a.rows[i] = -1;
 }
@@ -169,8 +198,7 @@ __device__ __forceinline__ int group_bits(int E) {
 // One row: the lane j < k gets choice j, its id and weight.  A row with a NaN or +infinity has no choices, and NaN for
 // weights.
 template <bool BF16, int EC>
-__device__ __forceinline__ void route_row(const RouteDev &a, int64_t t, int lane, int &id, float &w) {
-    RowKeys<EC> r = load_row_keys<BF16, EC>(a.logits, a.ld, a.E, t, lane);
+__device__ __forceinline__ void route_row(const RouteDev &a, RowKeys<EC> r, int lane, int &id, float &w) {
     const bool bad = row_bad(r);
     const float top = key_to_f32(row_max(r));
     float s = 0.0f;
@@ -179,16 +207,17 @@ __device__ __forceinline__ void route_row(const RouteDev &a, int64_t t, int lane
         for (int c = 0; c < EC; c++) s += r.k[c] > kKeyNegInf ? expf(key_to_f32(r.k[c]) - top) : 0.0f;
     }
     id = -1;
-    float p = 0.0f;
+    uint32_t mine = kKeyNegInf;
     for (int j = 0; j < a.k && !bad; j++) {
         uint32_t key;
         const int e = pop_max(r, lane, key);
         if (e < 0) break;
         if (lane == j) {
             id = e;
-            p = expf(key_to_f32(key) - top);
+            mine = key;
         }
     }
+    const float p = id >= 0 ? expf(key_to_f32(mine) - top) : 0.0f;
     const float den = wave_sum_f32(a.renorm ? p : s);
     w = bad ? __builtin_nanf("") : id >= 0 ? p / den : 0.0f;
 }
@@ -198,13 +227,17 @@ __global__ __launch_bounds__(kThreads) void k_mx_route(RouteDev a) {
     __shared__ SortShared s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t n0 = blockIdx.x * a.run, n = min(a.run, a.P - n0);
-    for (int j = tid; j < kWaves * a.E; j += kThreads) s.cnt[j / a.E][j % a.E] = 0;
-    __syncthreads();
+    clear_counts(a, s, lane, wave);
     const int64_t t1 = (n0 + n) / a.k;
-    for (int64_t t = n0 / a.k + wave; t < t1; t += kWaves) {
+    int64_t t = n0 / a.k + wave;
+    RowKeys<EC> next;
+    if (t < t1) next = load_row_keys<BF16, EC>(a.logits, a.ld, a.E, t, lane);
+    for (; t < t1; t += kWaves) {
+        const RowKeys<EC> row = next;
+        if (t + kWaves < t1) next = load_row_keys<BF16, EC>(a.logits, a.ld, a.E, t + kWaves, lane);
         int id;
         float w;
-        route_row<BF16, EC>(a, t, lane, id, w);
+        route_row<BF16, EC>(a, row, lane, id, w);
         if (lane < a.k) {
             a.out_ids[t * a.k + lane] = id;
             a.weights[t * a.k + lane] = w;
@@ -381,8 +414,9 @@ hipError_t launch_mx_route(const MxRouteArgs &p, void *workspace, hipStream_t st
 }
 
 hipError_t launch_mx_sort(const int32_t *ids, int64_t rows, int per_row, int64_t groups, int32_t *offsets, int32_t *out_rows,
-                          int32_t *places, void *workspace, hipStream_t stream) {
+                          int32_t *places, bool rest, void *workspace, hipStream_t stream) {
     RouteDev a{};
+    a.rest = rest;
     a.T = rows;
     a.P = rows * per_row;
     a.E = (int)groups;

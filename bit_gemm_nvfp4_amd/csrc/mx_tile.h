@@ -4,7 +4,6 @@
 #pragma once
 
 #include "mx.h"
-#include "mx_adapters.h"
 #include "mx_bounds.h"
 #include "mx_plan.h"
 
@@ -356,9 +355,10 @@ __device__ __forceinline__ void mx_tile_product(uint8_t *lds, int kb, int w0, in
 
 // The wave's sums to C: its corner is (mw, nw) of the M x N matrix c; `wide` where all its columns are there and 16-byte
 // stores are aligned.
-template <class T, class OT>
+// row_of(m, i, r): the row of c that row m is, row r of the wave's row tile i; asked by whole waves.
+template <class T, class OT, class Row>
 __device__ __forceinline__ void mx_store_tile(uint8_t *lds, const f32x16 (&acc)[T::TM][T::TN], OT *c, int64_t ldc, int64_t mw,
-                                              int64_t M, int64_t nw, int64_t N, bool wide) {
+                                              int64_t M, int64_t nw, int64_t N, bool wide, Row row_of) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     constexpr int VEC = 16 / sizeof(OT);
     // Each lane holds single elements of many rows (column l % 32), and a store instruction takes 16
@@ -380,15 +380,15 @@ __device__ __forceinline__ void mx_store_tile(uint8_t *lds, const f32x16 (&acc)[
             for (int q = 0; q < 32 / RPI; q++) {
                 const int row = q * RPI + lane / LPR, col = lane % LPR * VEC;
                 const float *src = buf + row * T::EPI_ROW + col;
-                const int64_t m = mw + 32 * i + row;
+                const int64_t m = mw + 32 * i + row, to = row_of(m, i, row);
                 if constexpr (VEC == 4) {
                     const f32x4 v = *reinterpret_cast<const f32x4 *>(src);
-                    if (m < M) *reinterpret_cast<f32x4 *>(c + m * ldc + nw + col) = v;
+                    if (m < M) *reinterpret_cast<f32x4 *>(c + to * ldc + nw + col) = v;
                 } else {
                     const f32x4 u = *reinterpret_cast<const f32x4 *>(src), w = *reinterpret_cast<const f32x4 *>(src + 4);
                     const bf16x8 v{(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
                                    (__bf16)w[0], (__bf16)w[1], (__bf16)w[2], (__bf16)w[3]};
-                    if (m < M) *reinterpret_cast<bf16x8 *>(c + m * ldc + nw + col) = v;
+                    if (m < M) *reinterpret_cast<bf16x8 *>(c + to * ldc + nw + col) = v;
                 }
             }
         }
@@ -398,12 +398,14 @@ __device__ __forceinline__ void mx_store_tile(uint8_t *lds, const f32x16 (&acc)[
     for (int i = 0; i < T::TM; i++)
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-            const int64_t m = mw + 32 * i + 8 * (e / 4) + 4 * h + e % 4;
+            const int row = 8 * (e / 4) + 4 * h + e % 4;
+            const int64_t m = mw + 32 * i + row, at = row_of(m, i, row);
             if (m >= M) continue;
+            OT *const to = c + at * ldc;
 #pragma unroll
             for (int j = 0; j < T::TN; j++) {
                 const int64_t n = nw + 32 * j + (lane & 31);
-                if (n < N) store_out(c + m * ldc + n, acc[i][j][e]);
+                if (n < N) store_out(to + n, acc[i][j][e]);
             }
         }
 }
@@ -419,16 +421,10 @@ struct MxTileArgs {
     int tiles_m, tiles_n;
     int slice_windows;  // windows of 512 columns per K slice (blockIdx.y)
     int vec_c;          // rows of C (of the partial planes) are 16-byte aligned
-    static constexpr bool kAdapters = false;
 };
 
-struct MxAdapterTileArgs : MxTileArgs {
-    Adapters ad;
-    static constexpr bool kAdapters = true;
-};
-
-template <class T, class OT, bool SPLIT, class Args>
-__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(Args p) {
+template <class T, class OT, bool SPLIT>
+__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_tile(MxTileArgs p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
     int tm, tn;
     if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn)) return;
@@ -490,12 +486,68 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     if constexpr (SPLIT) c += (int64_t)blockIdx.y * p.M * p.N;
     const int64_t ldc = SPLIT ? p.N : p.ldc;
     const int64_t mw = m0 + (wave / T::WN) * T::WTM, nw = n0 + (wave % T::WN) * T::WTN;  // the wave's corner
-    if constexpr (Args::kAdapters) {
-        // Of K slices the first has the branch.  (The question stands here without slices too: without it the largest
-        // tile's main loop and the branch share a block of code, and 88 registers a lane go to memory.)
-        if (blockIdx.y == 0) add_adapters<T::TM, T::TN>(p.ad, acc, mw, p.M, nw, p.N);
+    mx_store_tile<T>(lds, acc, c, ldc, mw, p.M, nw, p.N, n0 + T::BN <= p.N && p.vec_c, [](int64_t m, int, int) { return m; });
+}
+
+// The operands of a tile whose rows are picked: a_row(r) and w_row(r) are the rows of tile row r in A and in W, counted from
+// a and w, or -1 for none.  Rows lie within a_bytes and w_bytes (below 2^31) of them.
+struct MxPicked {
+    const uint8_t *a, *ascales;
+    uint32_t a_bytes;
+    int a_row_bytes, a_row_len;
+    const uint8_t *w, *wscales;
+    uint32_t w_bytes;
+    int K;
+};
+
+// acc += the product over windows w0 .. w1 - 1 of the tile.
+template <class T, class ARow, class WRow>
+__device__ __forceinline__ void mx_picked_product(uint8_t *lds, const MxPicked &p, int w0, int w1, ARow a_row, WRow w_row,
+                                                  f32x16 (&acc)[T::TM][T::TN]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kb = p.K / kMxBlock, wrb = p.K / 2, arb = p.a_row_bytes, alen = p.a_row_len;
+    const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(p.a, p.a_bytes), rw = uniform_rsrc(p.w, p.w_bytes);
+    const uint32_t abytes = (uint32_t)__builtin_amdgcn_readfirstlane(p.a_bytes),
+                   wbytes = (uint32_t)__builtin_amdgcn_readfirstlane(p.w_bytes);
+    // Direct-to-LDS loads: unit u = wave + NW i fills 1 KiB of a stage (8 rows of 128 bytes, or 32 of 32).  Every
+    // lane's offset is its own row's; those without a row, and pieces past the end of a row, lie past the buffers'
+    // ranges and load zeros.
+    constexpr int A_PER = T::A_UNITS / T::NW, RPU = 64 / T::W_PIECES;
+    const int ar = wave * 8 + lane / 8, wr = wave * RPU + lane / T::W_PIECES;
+    const int apb = swizzle<8>(ar, lane % 8) * 16, wpb = swizzle<T::W_PIECES>(wr, lane % T::W_PIECES) * 16;
+    uint32_t off[T::UPW];
+#pragma unroll
+    for (int i = 0; i < T::UPW; i++) {
+        const int r = i < A_PER ? a_row(i * (T::NW * 8) + ar) : w_row((i - A_PER) * (T::NW * RPU) + wr);
+        off[i] = bounds::row_off(r, i < A_PER ? arb : wrb, i < A_PER ? apb : wpb);
     }
-    mx_store_tile<T>(lds, acc, c, ldc, mw, p.M, nw, p.N, n0 + T::BN <= p.N && p.vec_c);
+    const int step0 = w0 * T::WINDOW_STEPS;
+    auto load_stage = [&](int s) {
+        uint8_t *dst = lds + (s % T::NST) * T::STAGE + wave * 1024;
+        const int ao = (step0 + s) * T::A_ROWB, wo = (step0 + s) * T::W_ROWB;
+        const uint32_t as = bounds::part_soff(ao, abytes), ws = bounds::part_soff(wo, wbytes);
+#pragma unroll
+        for (int i = 0; i < T::UPW; i++)
+            load_to_lds16(i < A_PER ? ra : rw, dst + i * (T::NW * 1024),
+                          i < A_PER ? bounds::step_off(off[i], ao, apb, alen) : bounds::step_off(off[i], wo, wpb, wrb),
+                          i < A_PER ? as : ws);
+    };
+    const uint8_t *srow[T::SC_PER];
+#pragma unroll
+    for (int i = 0; i < T::SC_PER; i++) {
+        const int r = tid + i * T::NT;
+        srow[i] = nullptr;
+        if (r < T::SA_ROWS) {
+            const int s = a_row(r);
+            if (s >= 0) srow[i] = p.ascales + (int64_t)s * kb;
+        } else if (r < T::SC_ROWS) {
+            const int s = w_row(r - T::SA_ROWS);
+            if (s >= 0) srow[i] = p.wscales + (int64_t)s * kb;
+        }
+    }
+    const int windows = (p.K + kGroup - 1) / kGroup;
+    const int nsteps = min((w1 - w0) * T::WINDOW_STEPS, (p.K + T::BK - 1) / T::BK - step0);
+    mx_tile_product<T>(lds, kb, w0, windows, nsteps, srow, load_stage, acc);
 }
 
 }  // namespace nvfp4

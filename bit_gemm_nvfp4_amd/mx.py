@@ -45,7 +45,7 @@ _SIGNATURES.update({
                       _P],
     "mxfp4_experts_workspace_size": [_I64, _I64, _I32, _I64, _I64, _I32, _I32],
     "mxfp4_gemm_adapters": [_P, _PX, _I64, _I64, _PX, _P, _I64, _I64, _P, _P, _P, _P, _I32, _I64, _P, _SZ, _P],
-    "mxfp4_adapters_workspace_size": [_I64, _I64, _I64, _I64, _I32],
+    "mxfp4_adapters_workspace_size": [_I64, _I64, _I64, _I64, _I64, _I32],
 })
 for _name in ("mxfp4_workspace_size", "mxfp4_experts_workspace_size", "mxfp4_adapters_workspace_size"):
     _RESTYPES[_name] = _SZ
@@ -413,11 +413,11 @@ def mx_experts(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_
     return (out, ids, weights) if routing else out
 
 
-def mx_adapters_workspace(m: int, w: MXFP4Tensor, rank: int, quantized_acts: bool = False) -> torch.Tensor | None:
-    """A workspace for mx_gemm_adapters with m rows (None without any).  Its contents do not matter; calls that share one
+def mx_adapters_workspace(m: int, w: MXFP4Tensor, adapters: int, rank: int, quantized_acts: bool = False) -> torch.Tensor | None:
+    """A workspace for mx_gemm_adapters with m rows (None when it needs none).  Its contents do not matter; calls that share one
     must be ordered (same stream, or events)."""
     dev = w.codes.device
-    args = (m, w.shape[0], w.shape[1], rank, 1 if quantized_acts else 0)
+    args = (m, w.shape[0], w.shape[1], adapters, rank, 1 if quantized_acts else 0)
     if dev.index == _current_device():  # the size is planned for the current device
         return _workspace(int(load_library().mxfp4_adapters_workspace_size(*args)), dev)
     with torch.cuda.device(dev.index):
@@ -449,7 +449,7 @@ def mx_gemm_adapters(a: torch.Tensor, w: MXFP4Tensor, down: torch.Tensor, up: to
     scales_ptr = None if scales is None else _words(scales, "scales", dev, torch.float32, count)
     out, ldc, dt = _out(out, m, n, dtype, dev, "out")
     if workspace is None:
-        workspace = mx_adapters_workspace(m, w, rank, a_q is not None)
+        workspace = mx_adapters_workspace(m, w, count, rank, a_q is not None)
     _call("mxfp4_gemm_adapters", dev, a.data_ptr(), a_ct, m, lda, ctypes.byref(w.c()), index_ptr, count, rank, down_ptr, up_ptr,
           scales_ptr, out.data_ptr(), dt, ldc, _opt(workspace, dev, "workspace"), _nbytes(workspace))
     return out

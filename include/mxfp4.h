@@ -223,15 +223,15 @@ enum { MXFP4_MAX_ADAPTERS = 1 << 16, MXFP4_MAX_RANK = 256 };
  * Sums are fp32 (A . V^T too, which passes on with fp32's 24 bits), and C is rounded once.  What an adapter holds reaches
  * the rows that name it and no others.  A NaN or infinity in V or U gives NaN or infinity in rows that name that adapter.
  * index, down, up and scales are read on the device.
- * workspace (16-byte aligned): at least M * rank * 4 bytes, rounded up to 256 (NVFP4_ERR_WORKSPACE for less; none without
- * adapters); with mxfp4_adapters_workspace_size(...) bytes a long K may be split as in mxfp4_gemm.  quantized_acts: whether
- * a_q is given.  M <= MXFP4_GROUP_MAX_ROWS; else limits and errors as for mxfp4_gemm.
+ * workspace (16-byte aligned; none without adapters): with mxfp4_adapters_workspace_size(...) bytes a long K may be split as
+ * in mxfp4_gemm; what that size is for K = 32 is needed in any case (NVFP4_ERR_WORKSPACE for less).  quantized_acts: whether
+ * a_q is given.  M <= MXFP4_GROUP_MAX_ROWS, lda <= 2^22; else limits and errors as for mxfp4_gemm.
  */
 nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                                  const int32_t *index, int64_t adapters, int64_t rank, const void *down, const void *up,
                                  const float *scales, void *c, nvfp4_dtype c_dtype, int64_t ldc, void *workspace,
                                  size_t workspace_bytes, hipStream_t stream);
-size_t mxfp4_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int quantized_acts);
+size_t mxfp4_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank, int quantized_acts);
 
 /* Workspace bytes of an entry point (0 when none); see the selectors for the arguments.  Planned for
  * the current device (an MI355X's 256 CUs when none can be queried). */

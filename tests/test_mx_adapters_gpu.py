@@ -44,7 +44,8 @@ def expected(nv, a, w, down, up, scales, index, a_q=None):
     # fp32 sums of products: a partial sum is at most the sum of the magnitudes and is rounded at most once per eight
     # products, and 16 more times in the joins of waves and slices
     steps = (k / 8 + 16) * 2.0 ** -24
-    y, err = main @ wd.t(), steps * (main.abs() @ wd.abs().t())
+    mag = main.abs() @ wd.abs().t()
+    y, err = main @ wd.t(), steps * mag
     for j in torch.unique(index).tolist():
         if not 0 <= j < down.shape[0]:
             continue
@@ -54,8 +55,10 @@ def expected(nv, a, w, down, up, scales, index, a_q=None):
         t, dt = s * (xr @ v.t()), s * steps * (xr.abs() @ v.abs().t())
         dt = dt + 2.0 ** -23 * t.abs()  # the scale
         y[rows] += t @ u.t()
-        # the up product: at worst a rounding for each product and each sum, and one where the branch joins
-        err[rows] += dt @ u.abs().t() + (2 * rank + 8) * 2.0 ** -24 * ((t.abs() + dt) @ u.abs().t())
+        # the up product, at worst: for few rows a rounding for each product and each sum of its own; for many it goes on the
+        # product's sums, three planes of T one after the other, with a rounding per eight ranks of each
+        tu = (t.abs() + dt) @ u.abs().t()
+        err[rows] += dt @ u.abs().t() + (2 * rank + 8) * 2.0 ** -24 * tu + (3 * rank / 8 + 8) * 2.0 ** -24 * (mag[rows] + tu)
     return y, err + 2.0 ** -23 * y.abs()
 
 
@@ -94,8 +97,8 @@ def test_every_tile_shape(nv, shape, act, tile, splits):
     for dt in TDT.values():
         check(nv.mx_gemm_adapters(a, w, down, up, index, scales=scales, a_q=a_q, dtype=dt), want, err, dt)
     # unsplit, with a workspace for T alone
-    t_bytes = (m * 24 * 4 + 255) // 256 * 256
-    ws = torch.empty(t_bytes, dtype=torch.uint8, device=DEV)
+    least = nv.lib.mxfp4_adapters_workspace_size(m, n, 32, 5, 24, act == "mx")
+    ws = torch.empty(least, dtype=torch.uint8, device=DEV)
     check(nv.mx_gemm_adapters(a, w, down, up, index, scales=scales, a_q=a_q, workspace=ws), want, err, torch.float32)
 
 

@@ -157,8 +157,9 @@ def test_binding_refusals(nv):
 def test_adapters_refusals(nv):
     size = nv.lib.mxfp4_adapters_workspace_size
     M, N, K, R, C = 100, 64, 128, 16, 3
-    ws = size(M, N, K, R, 0)
-    assert ws >= M * R * 4 and size(0, N, K, R, 0) == 0 and size(M, N, K, 12, 0) == 0 and size(MAX_ROWS + 1, N, K, R, 0) == 0
+    ws = size(M, N, K, C, R, 0)
+    assert ws >= M * R * 6 + M * 4 and size(16, N, K, C, R, 0) >= 16 * R * 4 and size(M, N, K, 0, R, 0) == 0  # T; the rows' order
+    assert size(0, N, K, C, R, 0) == 0 and size(M, N, K, C, 12, 0) == 0 and size(MAX_ROWS + 1, N, K, C, R, 0) == 0
 
     def call(a16=P(FAKE), aq=None, m=M, lda=K, wt=_mx(N, K), idx=P(FAKE), cnt=C, r=R, dn=P(FAKE), up=P(FAKE), sc=None, c=P(FAKE), dt=0,
              ldc=N, w=P(FAKE), wsb=ws):
@@ -173,7 +174,7 @@ def test_adapters_refusals(nv):
     assert call(aq=_mx(M - 1, K)) == 2 and call(aq=_mx(M, K + 32)) == 2
     assert call(lda=132) == 3 and call(dn=P(FAKE + 8)) == 3 and call(up=P(FAKE + 8)) == 3 and call(idx=P(FAKE + 2)) == 3
     assert call(sc=P(FAKE + 2)) == 3 and call(c=P(FAKE + 2)) == 3 and call(w=P(FAKE + 8)) == 3
-    need = (M * R * 4 + 255) // 256 * 256
+    need = size(M, N, 32, C, R, 0)
     assert call(w=None) == 5 and call(wsb=need - 1) == 5
     if not _gpu():
         assert call() == 7 and call(wsb=need) == 7 and call(cnt=0, dn=None, up=None, w=None) == 7 and call(aq=_mx(M, K)) == 7
