@@ -6,8 +6,8 @@
 // k_mx_count, k_mx_place: a counting sort of the (row, choice) pairs by group, stable in the pairs' order.  A
 //   workgroup has a run of pairs; its counts per group (k_mx_route makes them as it goes, k_mx_count for choices that
 //   are given) go to the workspace, and k_mx_place adds up those of the workgroups before its own, so that every pair's
-//   place follows from counts alone.  Nothing is made by atomics, so the order never depends on timing.  Up to
-//   kOneBlockRows rows one workgroup does both parts in one launch.
+//   place follows from counts alone.  Nothing is made by atomics, so the order never depends on timing.  Few rows are
+//   done by one workgroup in one launch.
 // k_mx_combine: y[t] = sum_j w[t][j] z[places[t][j]] in fp32, in the order of j.  Bound by reading z.
 #include <hip/hip_runtime.h>
 
@@ -24,7 +24,9 @@ namespace {
 constexpr int kMaxG = MXFP4_MOE_MAX_EXPERTS;
 constexpr int kWaves = 16, kThreads = 64 * kWaves;
 constexpr int kMaxBlocks = 256;      // runs of pairs
-constexpr int kOneBlockRows = 64;    // rows of logits that one workgroup routes and sorts
+// Rows of logits that one workgroup routes and sorts in one launch, a row per wave: 16 x 64 6.8 us, in two launches 9; 64 x 64
+// 13.6 and 9.1.
+constexpr int kOneBlockRows = 16;
 constexpr int kOneBlockPairs = 4096; // given choices that one workgroup sorts
 
 struct RouteDev {

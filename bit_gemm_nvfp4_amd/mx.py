@@ -7,6 +7,7 @@ A thin ctypes binding over the entry points of ``include/mxfp4.h``; the package 
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -19,6 +20,7 @@ MX_BLOCK = 32
 SKINNY_MAX_M = 16  # products of up to this many rows take no workspace
 MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 64, 512, 16
 GROUP_MAX_ROWS, MAX_GROUPS = 1 << 24, MOE_MAX_EXPERTS
+ROUTE_ONE_LAUNCH = 16  # a router of up to this many rows takes no workspace
 MX_EXPORTED = ["mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_moe", "mxfp4_workspace_size", "mxfp4_route",
                "mxfp4_group_rows", "mxfp4_grouped_gemm", "mxfp4_combine", "mxfp4_experts",
                "mxfp4_experts_workspace_size", "mxfp4_gemm_adapters", "mxfp4_adapters_workspace_size"]
@@ -273,9 +275,9 @@ class Grouping:
 
 def _words(t: torch.Tensor, what: str, device: torch.device, dtype: torch.dtype, *shape) -> int:
     """Address of a dense tensor argument of the given type and shape."""
-    assert t.device == device and t.dtype is dtype and tuple(t.shape) == shape and t.is_contiguous(), \
-        f"{what}: a dense {dtype} tensor {shape} on {device} is required, not {tuple(t.shape)} {t.dtype} on {t.device}"
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise AssertionError(f"{what}: a dense {dtype} tensor {shape} on {device} is required, not {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 def mx_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
@@ -290,10 +292,11 @@ def mx_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
     t, e = logits.shape
     assert top_k >= 1, f"top_k: at least 1, not {top_k}"
     n = t * top_k
-    words = torch.empty(3 * n + e + 1, dtype=torch.int32, device=dev)  # one allocation
-    ids, places, rows, offsets = words[:n].view(t, top_k), words[n:2 * n].view(t, top_k), words[2 * n:3 * n], words[3 * n:]
+    # (one allocation, divided)
+    ids, places, rows, offsets = torch.empty(3 * n + e + 1, dtype=torch.int32, device=dev).split((n, n, n, e + 1))
+    ids, places = ids.view(t, top_k), places.view(t, top_k)
     weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
-    if workspace is None:
+    if workspace is None and t > ROUTE_ONE_LAUNCH:  # none needed below
         workspace = _workspace(mx_workspace_size(MX_OP_ROUTE, t, top_k, e), dev)
     _call("mxfp4_route", dev, logits.data_ptr(), _DT[logits.dtype], t, ld, e, top_k, 1 if renormalize else 0, ids.data_ptr(),
           weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), places.data_ptr(), _opt(workspace, dev, "workspace"),
@@ -413,15 +416,22 @@ def mx_experts(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_
     return (out, ids, weights) if routing else out
 
 
+@functools.lru_cache(maxsize=256)
+def _adapters_size(device: int, *args) -> int:
+    """Bytes of a workspace, which are planned for the current device.  (A call into the library takes as long as the rest of
+    the binding's checks.)"""
+    if device == _current_device():
+        return int(load_library().mxfp4_adapters_workspace_size(*args))
+    with torch.cuda.device(device):
+        return int(load_library().mxfp4_adapters_workspace_size(*args))
+
+
 def mx_adapters_workspace(m: int, w: MXFP4Tensor, adapters: int, rank: int, quantized_acts: bool = False) -> torch.Tensor | None:
     """A workspace for mx_gemm_adapters with m rows (None when it needs none).  Its contents do not matter; calls that share one
     must be ordered (same stream, or events)."""
     dev = w.codes.device
-    args = (m, w.shape[0], w.shape[1], adapters, rank, 1 if quantized_acts else 0)
-    if dev.index == _current_device():  # the size is planned for the current device
-        return _workspace(int(load_library().mxfp4_adapters_workspace_size(*args)), dev)
-    with torch.cuda.device(dev.index):
-        return _workspace(int(load_library().mxfp4_adapters_workspace_size(*args)), dev)
+    n, k = w.shape
+    return _workspace(_adapters_size(dev.index, m, n, k, adapters, rank, 1 if quantized_acts else 0), dev)
 
 
 def mx_gemm_adapters(a: torch.Tensor, w: MXFP4Tensor, down: torch.Tensor, up: torch.Tensor, index: torch.Tensor,

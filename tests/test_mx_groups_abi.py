@@ -31,8 +31,8 @@ def _gpu():
 
 def test_workspace_sizes(nv):
     from bit_gemm_nvfp4_amd import mx
-    assert nv.mx_workspace_size(mx.MX_OP_ROUTE, 64, 8, 512) == 0            # one workgroup
-    assert nv.mx_workspace_size(mx.MX_OP_ROUTE, 65, 8, 512) == 5 * 512 * 4  # a table of counts: 16 rows a workgroup,
+    assert mx.ROUTE_ONE_LAUNCH == 16 and nv.mx_workspace_size(mx.MX_OP_ROUTE, 16, 8, 512) == 0  # one workgroup
+    assert nv.mx_workspace_size(mx.MX_OP_ROUTE, 17, 8, 512) == 2 * 512 * 4  # a table of counts: 16 rows a workgroup,
     assert nv.mx_workspace_size(mx.MX_OP_ROUTE, 1 << 20, 16, 512) == 256 * 512 * 4  # never more than 256
     assert nv.mx_workspace_size(mx.MX_OP_GROUP_ROWS, 4096, 1, 40) == 0
     assert nv.mx_workspace_size(mx.MX_OP_GROUP_ROWS, 4097, 1, 40) == 2 * 40 * 4
@@ -63,7 +63,7 @@ def test_route_refusals(nv):
         assert call(**{name: P(FAKE + 2)}) == 3
     assert call(w=P(FAKE + 8)) == 3 and call(w=None) == 5 and call(wsb=ws - 1) == 5
     if not _gpu():
-        assert call() == 7 and call(t=64, w=None) == 7 and call(t=0, lg=None, ids=None, wt=None, rows=None, pl=None, w=None) == 7
+        assert call() == 7 and call(t=16, w=None) == 7 and call(t=0, lg=None, ids=None, wt=None, rows=None, pl=None, w=None) == 7
 
 
 def test_group_rows_refusals(nv):

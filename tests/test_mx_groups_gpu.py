@@ -63,8 +63,8 @@ def check_sort(r, ids, groups):
     assert np.array_equal(r.places.cpu().numpy(), places)
 
 
-# one workgroup up to 64 rows, then 16 rows a workgroup, more from 4096 rows on; 64, 128, 256 and 512 experts to a row
-@pytest.mark.parametrize("t, e, k", [(1, 1, 1), (1, 64, 8), (3, 65, 2), (17, 5, 5), (64, 128, 16), (65, 130, 3), (300, 512, 16),
+# one workgroup up to 16 rows, then 16 rows a workgroup, more from 4096 rows on; 64, 128, 256 and 512 experts to a row
+@pytest.mark.parametrize("t, e, k", [(1, 1, 1), (1, 64, 8), (3, 65, 2), (16, 40, 3), (17, 5, 5), (64, 128, 16), (65, 130, 3), (300, 512, 16),
                                      (1000, 257, 6), (4096, 40, 1), (4097, 7, 2), (9000, 33, 4)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("renorm", [True, False])
