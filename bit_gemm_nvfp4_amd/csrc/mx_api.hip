@@ -54,6 +54,12 @@ nvfp4_status check_rows(const void *p, int64_t rows, int64_t cols, int64_t ld, i
 
 // Products grouped by rows: rows of A and W short enough for the 256 that share a buffer to stay within 2^29 bytes.
 constexpr int64_t kMaxGroupK = (int64_t)1 << 20, kMaxGroupN = (int64_t)1 << 24;
+constexpr int64_t kMaxAdapterLd = (int64_t)1 << 21;  // (2^30 bytes)
+
+// Whether the tiles of a grouped product fit one launch.
+bool grouped_fits(int64_t rows, int64_t groups, int64_t N, int64_t K, bool a_mx, int cus) {
+    return rows == 0 || N == 0 || plan_grouped(rows, groups, N, K, a_mx, cus) >= 0;
+}
 
 bool pairs_fit(int64_t rows, int64_t per) {
     return rows >= 0 && per >= 0 && (per == 0 || rows <= MXFP4_GROUP_MAX_ROWS / per);
@@ -314,6 +320,7 @@ nvfp4_status mxfp4_grouped_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int
     if (st != NVFP4_OK) return st;
     const int cus = current_device_cus();
     if (cus == 0) return NVFP4_ERR_DEVICE;
+    if (!grouped_fits(rows, groups, w->rows / groups, K, a_q != nullptr, cus)) return NVFP4_ERR_SHAPE;
     if (rows == 0 || cols == 0) return NVFP4_OK;
     const MxGroupedArgs a{a_bf16, a_q, a_rows, lda, map, offsets, groups, rows, w, swiglu == 1, c, c_dtype, ldc, c_q};
     return launched(launch_mx_grouped(a, cus, stream));
@@ -372,6 +379,9 @@ nvfp4_status mxfp4_experts(const void *x, int64_t tokens, int64_t ld_x, const vo
     if (at.total > (workspace ? workspace_bytes : 0)) return NVFP4_ERR_WORKSPACE;
     const int cus = current_device_cus();
     if (cus == 0) return NVFP4_ERR_DEVICE;
+    if (!grouped_fits(tokens * top_k, experts, 2 * I, H, quantize_acts == 1, cus) ||
+        !grouped_fits(tokens * top_k, experts, H, I, quantize_acts == 1, cus))
+        return NVFP4_ERR_SHAPE;
     if (tokens == 0) return NVFP4_OK;
 
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
@@ -441,7 +451,7 @@ nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, in
         return NVFP4_ERR_SHAPE;
     st = check_rows(a_bf16, M, K, lda, 2, 16);
     if (st != NVFP4_OK) return st;
-    if (lda > kMaxTileLd) return NVFP4_ERR_SHAPE;
+    if (lda > kMaxAdapterLd) return NVFP4_ERR_SHAPE;
     if (a_q) {
         st = check_mx(a_q);
         if (st != NVFP4_OK) return st;

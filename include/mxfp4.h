@@ -168,7 +168,8 @@ nvfp4_status mxfp4_group_rows(const int32_t *ids, int64_t tokens, int per_token,
  * W4A16 and W4A4 as for mxfp4_gemm.  No workspace.
  * Errors: NVFP4_ERR_SHAPE for rows or a_rows > MXFP4_GROUP_MAX_ROWS, groups < 1 or > MXFP4_MAX_GROUPS, K == 0, K or
  * lda above 2^20, w->rows not a multiple of groups (with swiglu: of 2 groups), N above 2^24, with a map a_rows rows of A
- * of 2^31 bytes or more, with swiglu N / 2 rows of W of 2^30 bytes or more, or operands that disagree.
+ * of 2^31 bytes or more, with swiglu N / 2 rows of W of 2^30 bytes or more, more output tiles than one launch holds, or
+ * operands that disagree.
  */
 nvfp4_status mxfp4_grouped_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int64_t a_rows, int64_t lda, const int32_t *map,
                                 const int32_t *offsets, int64_t groups, int64_t rows, const mxfp4_tensor *w, int swiglu,
@@ -225,7 +226,7 @@ enum { MXFP4_MAX_ADAPTERS = 1 << 16, MXFP4_MAX_RANK = 256 };
  * index, down, up and scales are read on the device.
  * workspace (16-byte aligned; none without adapters): with mxfp4_adapters_workspace_size(...) bytes a long K may be split as
  * in mxfp4_gemm; what that size is for K = 32 is needed in any case (NVFP4_ERR_WORKSPACE for less).  quantized_acts: whether
- * a_q is given.  M <= MXFP4_GROUP_MAX_ROWS, lda <= 2^22; else limits and errors as for mxfp4_gemm.
+ * a_q is given.  M <= MXFP4_GROUP_MAX_ROWS, lda <= 2^21; else limits and errors as for mxfp4_gemm.
  */
 nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, int64_t M, int64_t lda, const mxfp4_tensor *w,
                                  const int32_t *index, int64_t adapters, int64_t rank, const void *down, const void *up,

@@ -140,6 +140,19 @@ int main(int, char **v) {
         for (ll have : {1ll, (ll)bn, 2 * cols})
             for (ll r : {-1ll, 0ll, have / 2, have - 1}) lane(r, have, w_rowb, steps, nst, k / 2, k / 2);
     }
+    // the adapters' first product: chunks of 256 or 512 bytes of rows of A (its tile's own or picked from all) and of V
+    for (ll k : {32ll, 96ll, 544ll, 4128ll, 1ll << 21})
+        for (int rowb : {256, 512})
+            for (ll pad : {0ll, 8ll, (1ll << 21) - k}) {
+                const ll row_bytes = 2 * (k + pad), row_len = 2 * k;
+                const int steps = (int)((row_len + rowb - 1) / rowb);
+                for (ll have : {1ll, 16ll, 64ll, ((1ll << 31) - 1) / row_bytes})
+                    for (ll r : {-1ll, 0ll, have / 2, have - 1}) lane(r, have, rowb, steps, nst, row_bytes, row_len);
+            }
+    // T and U of a tile: 64 ranks at a time
+    for (ll rank = 8; rank <= 256; rank += 8)
+        for (ll have : {1ll, (ll)bm, (ll)bn})
+            for (ll r : {-1ll, 0ll, have / 2, have - 1}) lane(r, have, 128, (int)((rank + 63) / 64), 1, 2 * rank, 2 * rank);
     printf("%lld loads, %lld of them refused\n", loads, refused);
     return refused > 0 ? 0 : 1;
 }
