@@ -1,12 +1,13 @@
 // Router of a mixture-of-experts layer for any number of tokens, the sort of rows by group behind it, and the weighted
 // sum of what the groups give back (gfx950).
 //
-// k_mx_route: top-k choices and softmax weights of a row of logits, one wave per row: the row sits in registers as
-//   unsigned keys (mx_route.h) and gives its largest entry k times.
+// k_mx_route: top-k choices and softmax weights, four rows of logits per wave: a row sits in the registers of 16 lanes as
+//   unsigned keys and gives its largest entry k times.
 // k_mx_count, k_mx_place: a counting sort of the (row, choice) pairs by group, stable in the pairs' order.  A
 //   workgroup has a run of pairs; its counts per group (k_mx_route makes them as it goes, k_mx_count for choices that
 //   are given) go to the workspace, and k_mx_place adds up those of the workgroups before its own, so that every pair's
-//   place follows from counts alone.  Nothing is made by atomics, so the order never depends on timing.  Few rows are
+//   place follows from counts alone.  No place comes from an atomic (counts are integer sums), so the order never
+//   depends on timing.  Few rows are
 //   done by one workgroup in one launch.
 // k_mx_combine: y[t] = sum_j w[t][j] z[places[t][j]] in fp32, in the order of j.  Bound by reading z.
 #include <hip/hip_runtime.h>
@@ -197,12 +198,62 @@ __device__ __forceinline__ int group_bits(int E) {
     return 32 - __builtin_clz((unsigned)E);
 }
 
-// One row: the lane j < k gets choice j, its id and weight.  A row with a NaN or +infinity has no choices, and NaN for
-// weights.
+// Four rows of logits per wave, one per row of 16 lanes: lane l of it holds entries c * 16 + l as keys.  Entries past E and
+// masked ones are kKeyNegInf.  (A wave per row spends its instructions on one choice at a time: 16384 x 128, top 8, 15 us.)
+template <int EC>
+struct Keys16 {
+    uint32_t k[EC];
+};
+
 template <bool BF16, int EC>
-__device__ __forceinline__ void route_row(const RouteDev &a, RowKeys<EC> r, int lane, int &id, float &w) {
-    const bool bad = row_bad(r);
-    const float top = key_to_f32(row_max(r));
+__device__ __forceinline__ Keys16<EC> load_keys16(const RouteDev &a, int64_t t, int l) {
+    Keys16<EC> r;
+#pragma unroll
+    for (int c = 0; c < EC; c++) {
+        const int j = c * 16 + l;
+        const int64_t at = t * a.ld + min(j, a.E - 1);
+        float v;
+        if constexpr (BF16) v = (float)reinterpret_cast<const __bf16 *>(a.logits)[at];
+        else v = reinterpret_cast<const float *>(a.logits)[at];
+        r.k[c] = j < a.E ? key_of(v) : kKeyNegInf;
+    }
+    return r;
+}
+
+// Over the 16 lanes of a row, the result in all of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max(v, dpp_u32<kDppXor1>(v));
+    v = max(v, dpp_u32<kDppXor2>(v));
+    v = max(v, dpp_u32<kDppHalfMirror>(v));
+    return max(v, dpp_u32<kDppMirror>(v));
+}
+__device__ __forceinline__ uint32_t min16(uint32_t v) {
+    v = min(v, dpp_u32<kDppXor1>(v));
+    v = min(v, dpp_u32<kDppXor2>(v));
+    v = min(v, dpp_u32<kDppHalfMirror>(v));
+    return min(v, dpp_u32<kDppMirror>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+    v += u2f(dpp_u32<kDppXor1>(f2u(v)));
+    v += u2f(dpp_u32<kDppXor2>(f2u(v)));
+    v += u2f(dpp_u32<kDppHalfMirror>(f2u(v)));
+    return v + u2f(dpp_u32<kDppMirror>(f2u(v)));
+}
+
+// The rows of a wave: lane j < k of each gets its choice j, the id and weight.  A row with a NaN or +infinity has no choices,
+// and NaN for weights.
+template <int EC>
+__device__ __forceinline__ void route_rows(const RouteDev &a, Keys16<EC> r, int l, int &id, float &w) {
+    uint32_t hi = r.k[0], lo = r.k[0];
+#pragma unroll
+    for (int c = 1; c < EC; c++) {
+        hi = max(hi, r.k[c]);
+        lo = min(lo, r.k[c]);
+    }
+    hi = max16(hi);
+    // a NaN's key is above +infinity's or below -infinity's
+    const bool bad = hi >= kKeyPosInf || min16(lo) < kKeyNegInf;
+    const float top = key_to_f32(hi);
     float s = 0.0f;
     if (!a.renorm) {
 #pragma unroll
@@ -210,40 +261,50 @@ __device__ __forceinline__ void route_row(const RouteDev &a, RowKeys<EC> r, int 
     }
     id = -1;
     uint32_t mine = kKeyNegInf;
-    for (int j = 0; j < a.k && !bad; j++) {
-        uint32_t key;
-        const int e = pop_max(r, lane, key);
-        if (e < 0) break;
-        if (lane == j) {
-            id = e;
-            mine = key;
+    for (int j = 0; j < a.k; j++) {
+        uint32_t m = r.k[0];
+#pragma unroll
+        for (int c = 1; c < EC; c++) m = max(m, r.k[c]);
+        m = max16(m);
+        uint32_t at = 0xFFFFFFFFu;  // the lowest entry that holds it
+#pragma unroll
+        for (int c = EC - 1; c >= 0; c--) at = r.k[c] == m ? (uint32_t)(c * 16) + l : at;
+        at = min16(at);
+        if (l == j && m > kKeyNegInf) {
+            id = (int)at;
+            mine = m;
         }
+#pragma unroll
+        for (int c = 0; c < EC; c++) r.k[c] = at == (uint32_t)(c * 16) + l ? kKeyNegInf : r.k[c];
     }
-    const float p = id >= 0 ? expf(key_to_f32(mine) - top) : 0.0f;
-    const float den = wave_sum_f32(a.renorm ? p : s);
+    const float p = mine > kKeyNegInf ? expf(key_to_f32(mine) - top) : 0.0f;
+    const float den = sum16(a.renorm ? p : s);
     w = bad ? __builtin_nanf("") : id >= 0 ? p / den : 0.0f;
+    if (bad) id = -1;
 }
 
 template <bool BF16, int EC>
 __global__ __launch_bounds__(kThreads) void k_mx_route(RouteDev a) {
     __shared__ SortShared s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15;
     const int64_t n0 = blockIdx.x * a.run, n = min(a.run, a.P - n0);
     clear_counts(a, s, lane, wave);
-    const int64_t t1 = (n0 + n) / a.k;
-    int64_t t = n0 / a.k + wave;
-    RowKeys<EC> next;
-    if (t < t1) next = load_row_keys<BF16, EC>(a.logits, a.ld, a.E, t, lane);
-    for (; t < t1; t += kWaves) {
-        const RowKeys<EC> row = next;
-        if (t + kWaves < t1) next = load_row_keys<BF16, EC>(a.logits, a.ld, a.E, t + kWaves, lane);
+    // rows of a workgroup are dealt to the waves first
+    constexpr int ROWS = 4 * kWaves;
+    const int64_t t0 = n0 / a.k, t1 = t0 + n / a.k;
+    int64_t t = t0 + (lane >> 4) * kWaves + wave;
+    Keys16<EC> next;
+    if (t0 + wave < t1) next = load_keys16<BF16, EC>(a, min(t, t1 - 1), l);  // (rows behind the last repeat it)
+    for (int64_t f = t0 + wave; f < t1; f += ROWS, t += ROWS) {
+        const Keys16<EC> rows = next;
+        if (f + ROWS < t1) next = load_keys16<BF16, EC>(a, min(t + ROWS, t1 - 1), l);
         int id;
         float w;
-        route_row<BF16, EC>(a, row, lane, id, w);
-        if (lane < a.k) {
-            a.out_ids[t * a.k + lane] = id;
-            a.weights[t * a.k + lane] = w;
-            if (id >= 0) s.cnt[wave][id]++;  // a row's choices differ, and no other wave has this line
+        route_rows<EC>(a, rows, l, id, w);
+        if (l < a.k && t < t1) {
+            a.out_ids[t * a.k + l] = id;
+            a.weights[t * a.k + l] = w;
+            if (id >= 0) atomicAdd(&s.cnt[wave][id], 1u);  // rows of a wave may choose the same
         }
     }
     __syncthreads();
@@ -371,10 +432,10 @@ int64_t sort_blocks(int64_t pairs, int64_t &run) { return runs_of(pairs, kOneBlo
 template <bool BF16>
 void launch_route_t(const RouteDev &a, hipStream_t stream) {
     const dim3 grid((unsigned)a.blocks), block(kThreads);
-    if (a.E <= 64) hipLaunchKernelGGL((k_mx_route<BF16, 1>), grid, block, 0, stream, a);
-    else if (a.E <= 128) hipLaunchKernelGGL((k_mx_route<BF16, 2>), grid, block, 0, stream, a);
-    else if (a.E <= 256) hipLaunchKernelGGL((k_mx_route<BF16, 4>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((k_mx_route<BF16, 8>), grid, block, 0, stream, a);
+    if (a.E <= 64) hipLaunchKernelGGL((k_mx_route<BF16, 4>), grid, block, 0, stream, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((k_mx_route<BF16, 8>), grid, block, 0, stream, a);
+    else if (a.E <= 256) hipLaunchKernelGGL((k_mx_route<BF16, 16>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((k_mx_route<BF16, 32>), grid, block, 0, stream, a);
 }
 
 }  // namespace
