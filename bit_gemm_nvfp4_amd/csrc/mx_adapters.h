@@ -11,7 +11,8 @@
 //     rows in the order of their adapters, so that a tile has few, and takes one of them at a time: U of the tile's columns
 //     and T of its rows pass through LDS, 64 ranks at a time.  (Read straight from memory in the operand layout, pieces of
 //     16 bytes from 32 rows an instruction, the branch of 4096 x 4096, rank 64, took 20 us.)  T of the
-//     others' rows is zero then.
+//     others' rows is zero then.  4096 x 4096 x 4096 W4A4, rank 64, 7 requests: 54 us with the product, which takes 38 us alone
+//     (44 with rows in another order and no adapter).
 #pragma once
 
 #include "mx_tile.h"

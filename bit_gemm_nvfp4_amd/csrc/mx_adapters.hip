@@ -7,7 +7,8 @@
 // adapters are formed too and not stored.
 // (Read straight in the operand layout, 16-byte pieces of sixteen rows, a load of 1 KiB took about 70 cycles of the address
 // unit: 4096 x 4096, rank 64, 25 us; 1 x 4096, rank 16, 6.3 us.)
-// Few rows: bound by the latency of one pass over V (rank x K x 2 bytes per adapter).  Many: by A and V coming through L2.
+// Few rows: bound by the latency of one pass over V (rank x K x 2 bytes per adapter): 1 x 4096, rank 16 4.5 us, 48 rows of 64
+// adapters 6.8 us.  Many: by A and V coming through L2: 4096 x 4096, rank 64 16 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

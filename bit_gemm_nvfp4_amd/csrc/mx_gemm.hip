@@ -266,7 +266,7 @@ __global__ __launch_bounds__(512) void k_adapter_skinny(const __bf16 *__restrict
 // -------------------------------------------------------------------------------------------------
 // M > 16
 // -------------------------------------------------------------------------------------------------
-// (the kernel: mx_tile.h)
+// The kernels are in mx_tile.h (k_mx_tile) and mx_adapters.h (k_adapter_tile, the product with the adapters' branch).
 
 // C = the sum of the K slices' partial planes, in slice order.  VEC columns per thread (4 where rows of the
 // planes and of C allow); the slices' loads are issued together.  Bound by reading the planes.
