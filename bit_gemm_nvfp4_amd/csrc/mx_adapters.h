@@ -244,7 +244,7 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     const int w0 = (int)blockIdx.y * p.slice_windows, w1 = min(w0 + p.slice_windows, windows);
     const TileAdapters<T> of = tile_adapters<T>(p.ad, m0, mrows);
     f32x16 acc[T::TM][T::TN] = {};
-    mx_picked_product<T>(lds, picked, w0, w1, a_row, w_row, acc);
+    mx_picked_product<T, false>(lds, picked, w0, w1, a_row, w_row, acc);
 
     // Of K slices the first has the branch.  (The question stands here without slices too: without it the largest
     // tile's main loop and the branch share a block of code, and registers go to memory.)

@@ -16,8 +16,8 @@
 //     4096 157 us, 0.87 PFLOP/s: about 2.4 rounds of tiles, of which the last is not full, and last tiles of a group that
 //     are not.
 //   prompts, W4A4: a tile of 256 x 256 takes 3.2 us per 512 columns of K and 8 us for its first loads and its stores.
-//     32768 rows, 64 groups, 4096 x 2048 234 us, 2.35 PFLOP/s.  (A workgroup per CU that works through its tiles and issues
-//     the next one's first loads ahead of this one's stores took 236 us: all CUs store at a time, 33 MB a round, and the
+//     32768 rows, 64 groups, 4096 x 2048 229 us, 2.4 PFLOP/s.  (A workgroup per CU that works through its tiles and issues
+//     the next one's first loads ahead of this one's stores was no faster: all CUs store at a time, 33 MB a round, and the
 //     main loop's first wait is for these stores too.)
 #include <hip/hip_runtime.h>
 
@@ -176,7 +176,9 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
                           (uint32_t)(wrows * (K / 2)),
                           K};
     f32x16 acc[T::TM][T::TN] = {};
-    mx_picked_product<T>(lds, picked, 0, (K + kGroup - 1) / kGroup, a_row, w_row, acc);
+    // (streaming: 768 rows, 64 groups, 3000 x 4096 77.8 -> 73.1 us, 16384 rows 197 -> 186, 32768 x 4096 x 2048 240 -> 229; with W4A16,
+    // whose steps take a quarter of a line, 100 -> 166)
+    mx_picked_product<T, true>(lds, picked, 0, (K + kGroup - 1) / kGroup, a_row, w_row, acc);
 
     const int mw = wave / T::WN * T::WTM;
     if constexpr (SWIGLU) {

@@ -500,8 +500,14 @@ struct MxPicked {
     int K;
 };
 
-// acc += the product over windows w0 .. w1 - 1 of the tile.
-template <class T, class ARow, class WRow>
+// load_to_lds16 of lines that the caches let go first.
+__device__ __forceinline__ void stream_to_lds16(__amdgpu_buffer_rsrc_t r, void *lds, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, voff, soff, 0, 2);
+}
+
+// acc += the product over windows w0 .. w1 - 1 of the tile.  STREAM: W's lines go first where a step takes whole ones (MXFP4 A),
+// so that the lines of scale bytes, which eight windows share, stay in L2.
+template <class T, bool STREAM, class ARow, class WRow>
 __device__ __forceinline__ void mx_picked_product(uint8_t *lds, const MxPicked &p, int w0, int w1, ARow a_row, WRow w_row,
                                                   f32x16 (&acc)[T::TM][T::TN]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -528,9 +534,12 @@ __device__ __forceinline__ void mx_picked_product(uint8_t *lds, const MxPicked &
         const uint32_t as = bounds::part_soff(ao, abytes), ws = bounds::part_soff(wo, wbytes);
 #pragma unroll
         for (int i = 0; i < T::UPW; i++)
-            load_to_lds16(i < A_PER ? ra : rw, dst + i * (T::NW * 1024),
-                          i < A_PER ? bounds::step_off(off[i], ao, apb, alen) : bounds::step_off(off[i], wo, wpb, wrb),
-                          i < A_PER ? as : ws);
+            if (i < A_PER)
+                load_to_lds16(ra, dst + i * (T::NW * 1024), bounds::step_off(off[i], ao, apb, alen), as);
+            else if (STREAM && T::W_ROWB == 128)
+                stream_to_lds16(rw, dst + i * (T::NW * 1024), bounds::step_off(off[i], wo, wpb, wrb), ws);
+            else
+                load_to_lds16(rw, dst + i * (T::NW * 1024), bounds::step_off(off[i], wo, wpb, wrb), ws);
     };
     const uint8_t *srow[T::SC_PER];
 #pragma unroll
