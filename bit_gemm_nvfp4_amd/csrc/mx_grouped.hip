@@ -11,14 +11,14 @@
 // makes it from the fp32 value), without its halves ever being in memory.
 //
 // What bounds it, kernel times:
-//   a few rows per group: streaming the groups' W.  256 rows, 64 groups, 4096 x 1536, W4A16 49 us, 4.3 TB/s of W.
+//   a few rows per group: streaming the groups' W.  256 rows, 64 groups, 4096 x 1536, W4A16 50 us, 4.3 TB/s of W.
 //   prompts, W4A16: matrix instructions and the W expansion between them.  4096 rows, 16 groups, gate and up of 4096 x
 //     4096 157 us, 0.87 PFLOP/s: about 2.4 rounds of tiles, of which the last is not full, and last tiles of a group that
 //     are not.
 //   prompts, W4A4: a tile of 256 x 256 takes 3.2 us per 512 columns of K and 8 us for its first loads and its stores.
-//     32768 rows, 64 groups, 4096 x 2048 229 us, 2.4 PFLOP/s.  (A workgroup per CU that works through its tiles and issues
-//     the next one's first loads ahead of this one's stores was no faster: all CUs store at a time, 33 MB a round, and the
-//     main loop's first wait is for these stores too.)
+//     32768 rows, 64 groups, 4096 x 2048 230 to 243 us, 2.3 PFLOP/s.  (A workgroup per CU that works through its tiles
+//     and issues the next one's first loads ahead of this one's stores was no faster: all CUs store at a time, 33 MB a
+//     round, and the main loop's first wait is for these stores too.)
 #include <hip/hip_runtime.h>
 
 #include "internal.h"

@@ -11,7 +11,7 @@
 //   done by one workgroup in one launch.
 // k_mx_combine: y[t] = sum_j w[t][j] z[places[t][j]] in fp32, in the order of j.  Bound by reading z: 4096 x 4096, four rows
 //   each, bf16 28 us, 5.4 TB/s.
-// The router is bound by latency: 16 rows 6.8 us, 4096 x 64 6.4 + 7.2 us (two launches), 16384 x 128, top 8 9.0 + 7.8 us.
+// The router is bound by latency: 16 rows 6.8 us, 4096 x 64 6.4 + 7.2 us (two launches), 16384 x 128, top 8 7.8 + 8.1 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -179,8 +179,8 @@ nvfp4_status mxfp4_grouped_gemm(const void *a_bf16, const mxfp4_tensor *a_q, int
  * mxfp4_combine -- y[t] = sum_j weights[t][j] . z[places[t][j]]: the rows that a token's choices gave back, weighted, in
  * the order of j.  z [z_rows x cols] fp32 or bf16 (row stride ld_z), places and weights [tokens x top_k] dense, y
  * [tokens x cols] fp32 or bf16 (row stride ld_y).  Sums are fp32, rounded once.  A place outside 0 .. z_rows - 1 counts
- * as a row of zeros, so a NaN weight still gives NaN.  Rows of z need the alignment of their element only.  top_k >= 1 (NVFP4_ERR_ARG), tokens * top_k <=
- * MXFP4_GROUP_MAX_ROWS (NVFP4_ERR_SHAPE).
+ * as a row of zeros, so a NaN weight still gives NaN.  Rows of z need the alignment of their element only.  top_k >= 1
+ * (NVFP4_ERR_ARG), tokens * top_k <= MXFP4_GROUP_MAX_ROWS (NVFP4_ERR_SHAPE).
  */
 nvfp4_status mxfp4_combine(const void *z, nvfp4_dtype z_dtype, int64_t z_rows, int64_t ld_z, const int32_t *places,
                            const float *weights, int64_t tokens, int top_k, int64_t cols, void *y, nvfp4_dtype y_dtype,
