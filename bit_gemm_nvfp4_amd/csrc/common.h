@@ -146,6 +146,15 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
            (u2f(readlane_u32(f2u(v), 32)) + u2f(readlane_u32(f2u(v), 48)));
 }
 
+// What the lanes of a wave have stored to LDS is there for each other's loads behind this point, and their loads are done before
+// each other's stores behind it.  The LDS operations of a wave complete in order, so it costs no instruction; it keeps the
+// compiler from moving such accesses across.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // s_waitcnt immediate: wait until at most `vm` vector-memory and `lgkm` LDS operations are pending.
 constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | (7 << 4) | ((lgkm & 15) << 8) | ((vm >> 4) << 14); }
 

@@ -86,6 +86,7 @@ __device__ __forceinline__ int group_of(const RouteDev &a, int64_t i) {
 
 __device__ __forceinline__ void clear_counts(const RouteDev &a, SortShared &s, int lane, int wave) {
     for (int e = lane; e < a.E; e += 64) s.cnt[wave][e] = 0;  // a wave's own line
+    wave_exchange();
 }
 
 // The wave's pairs a block of kAhead x 64 at a time, their groups loaded side by side: each(place of the lane's pair, or -1
@@ -114,6 +115,7 @@ __device__ __forceinline__ void count_pairs(const RouteDev &a, SortShared &s, in
         const bool ok = (unsigned)g < (unsigned)a.E;
         const uint64_t m = same_group(g, ok, bits);
         if (ok && lane == __builtin_ctzll(m)) s.cnt[wave][g] += __popcll(m);
+        wave_exchange();
     });
     __syncthreads();
 }
@@ -184,10 +186,12 @@ __device__ void place_pairs(const RouteDev &a, SortShared &s, int block, int64_t
         const bool ok = (unsigned)g < (unsigned)a.E;
         const uint64_t m = same_group(g, ok, bits);
         int at = -1;
+        const uint32_t base = ok ? s.cnt[wave][g] : 0;
+        wave_exchange();  // all lanes of the group have read it
+        if (ok && lane == __builtin_ctzll(m)) s.cnt[wave][g] = base + __popcll(m);
+        wave_exchange();
         if (ok) {
-            const uint32_t base = s.cnt[wave][g];
             at = (int)(base + __popcll(m & ((1ull << lane) - 1)));
-            if (lane == __builtin_ctzll(m)) s.cnt[wave][g] = base + __popcll(m);
             a.rows[at] = a.k == 1 ? (int32_t)i : (int32_t)((uint32_t)i / (uint32_t)a.k);
         }
         if (i >= 0 && a.places) a.places[i] = at;
