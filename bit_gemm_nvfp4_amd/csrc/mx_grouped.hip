@@ -85,6 +85,7 @@ __device__ __forceinline__ void store_swiglu(uint8_t *lds, const f32x16 (&acc)[T
             const float g = acc[i][0][e], u = acc[i][1][e];
             buf[(8 * (e / 4) + 4 * h + e % 4) * ROW + (lane & 31)] = g / (1.0f + expf(-g)) * u;
         }
+        wave_exchange();
 #pragma unroll
         for (int q = 0; q < 2; q++) {  // sixteen rows, eight columns a lane
             const int r = 16 * q + lane / 4, c8 = lane % 4 * 8, m = mw + 32 * i + r, n = nw + c8;
@@ -115,6 +116,7 @@ __device__ __forceinline__ void store_swiglu(uint8_t *lds, const f32x16 (&acc)[T
                 }
             }
         }
+        wave_exchange();  // the next rows take their place
     }
 }
 

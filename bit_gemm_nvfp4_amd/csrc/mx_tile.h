@@ -375,6 +375,7 @@ __device__ __forceinline__ void mx_store_tile(uint8_t *lds, const f32x16 (&acc)[
 #pragma unroll
                 for (int j = 0; j < T::TN; j++)
                     buf[(8 * (e / 4) + 4 * h + e % 4) * T::EPI_ROW + 32 * j + (lane & 31)] = acc[i][j][e];
+            wave_exchange();
             constexpr int LPR = T::WTN / VEC, RPI = 64 / LPR;  // lanes per row, rows per instruction
 #pragma unroll
             for (int q = 0; q < 32 / RPI; q++) {
@@ -391,6 +392,7 @@ __device__ __forceinline__ void mx_store_tile(uint8_t *lds, const f32x16 (&acc)[
                     if (m < M) *reinterpret_cast<bf16x8 *>(c + to * ldc + nw + col) = v;
                 }
             }
+            wave_exchange();  // the next rows take their place
         }
         return;
     }

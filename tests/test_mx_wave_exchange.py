@@ -61,3 +61,27 @@ def test_the_walk_finds_the_ways_without_a_fence():
     bare = gfx_ir.Lds([ln for ln in CODE.splitlines() if "fence" not in ln])
     assert len(bare.unordered(counts("S"), counts("L"), same_block=False)) == 1
     assert f.offset("getelementptr inbounds nuw (i8, ptr addrspace(3) @lds, i32 32768), i32 %9") == 32768
+
+
+@pytest.fixture(scope="module")
+def compiled(tmp_path_factory):
+    done, tmp = {}, tmp_path_factory.mktemp("mx_wave_ir")
+
+    def get(source):
+        if source not in done:
+            done[source] = gfx_ir.functions(gfx_ir.compiled(tmp, source))
+        return done[source]
+    return get
+
+
+# Sums on their way to C: each wave writes rows of its own part of LDS, a value a lane, and reads them back as whole pieces.
+@pytest.mark.parametrize("source, name, many", [("mx_grouped.hip", "k_mx_grouped", 45), ("mx_gemm.hip", "k_mx_tile", 30),
+                                                ("mx_gemm.hip", "k_adapter_tile", 30)])
+def test_sums_on_their_way_to_c(compiled, source, name, many):
+    found = kernels(compiled(source), name)
+    assert len(found) == many
+    value, piece = lambda kind, ty, off: (kind, ty) == ("S", "float"), lambda kind, ty, off: (kind, ty) == ("L", "<4 x float>")
+    for kernel, f in found.items():
+        assert sum(value(*s) for body, _ in f.blocks.values() for s in f.steps(body)) >= 16, kernel
+        assert not f.unordered(value, piece, same_block=True), kernel
+        assert not f.unordered(piece, value, same_block=True), kernel
