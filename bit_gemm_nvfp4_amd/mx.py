@@ -359,6 +359,8 @@ def mx_grouped_gemm(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor, offsets: torc
         c_ct, c_ptr = None, out.data_ptr()
     _call("mxfp4_grouped_gemm", dev, a_ptr, a_ct, a.shape[0], lda, map_ptr, off_ptr, groups, m, ctypes.byref(w.c()),
           1 if swiglu else 0, c_ptr, dt, ldc, c_ct)
+    if c_ct is not None:
+        out.flags = None  # a word of an earlier mx_quantize does not speak for these values
     return out
 
 
