@@ -458,7 +458,7 @@ nvfp4_status mxfp4_gemm_adapters(const void *a_bf16, const mxfp4_tensor *a_q, in
         if (a_q->rows != M || a_q->cols != K) return NVFP4_ERR_SHAPE;
     }
     const int eb = elem_bytes(c_dtype);
-    st = first_of({check_rows(down, adapters * rank, K, K, 2, 16), check_rows(up, adapters, N * rank, N * rank, 2, 16),
+    st = first_of({check_rows(down, adapters * rank, K, K, 2, 16), check_rows(up, adapters * N, rank, rank, 2, 16),
                    check_rows(c, M, N, ldc, eb, eb), check_words(index, M > 0), check_words(scales, false)});
     if (st != NVFP4_OK) return st;
     if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
