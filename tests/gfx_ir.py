@@ -9,10 +9,10 @@ SYNC = re.compile(r"\bfence\b|llvm\.amdgcn\.s\.barrier")
 OPS = {"load": "L", "store": "S", "atomicrmw": "X", "cmpxchg": "X"}
 
 
-def compiled(tmp, source, *flags):
+def compiled(tmp, source):
     """Lines of the IR of a source of the library."""
     out = os.path.join(str(tmp), source + ".ll")
-    cmd = [build.HIPCC, *build.FLAGS, "-S", "-emit-llvm", "--offload-device-only", os.path.join(build.CSRC, source), "-o", out, *flags]
+    cmd = [build.HIPCC, *build.FLAGS, "-S", "-emit-llvm", "--offload-device-only", os.path.join(build.CSRC, source), "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     with open(out) as f:
