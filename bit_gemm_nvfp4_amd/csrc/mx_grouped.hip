@@ -42,6 +42,7 @@ struct GroupedDev {
     int64_t ldc;
     uint8_t *cscales;
     int tiles_n, max_tiles_m, vec_c;
+    bool stream;   // W passes the caches by (MXFP4 A)
 };
 
 // Rows lo .. hi - 1 of group g, whatever the offsets hold: within the rows of C.
@@ -120,7 +121,7 @@ __device__ __forceinline__ void store_swiglu(uint8_t *lds, const f32x16 (&acc)[T
     }
 }
 
-template <class T, class OT, bool SWIGLU>
+template <class T, class OT, bool SWIGLU, bool STREAM>
 __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_grouped(GroupedDev p) {
     __shared__ __align__(1024) uint8_t lds[T::LDS_BYTES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -178,9 +179,7 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
                           (uint32_t)(wrows * (K / 2)),
                           K};
     f32x16 acc[T::TM][T::TN] = {};
-    // (streaming: 768 rows, 64 groups, 3000 x 4096 77.8 -> 73.1 us, 16384 rows 197 -> 186, 32768 x 4096 x 2048 240 -> 229; with W4A16,
-    // whose steps take a quarter of a line, 100 -> 166)
-    mx_picked_product<T, true>(lds, picked, 0, (K + kGroup - 1) / kGroup, a_row, w_row, acc);
+    mx_picked_product<T, STREAM>(lds, picked, 0, (K + kGroup - 1) / kGroup, a_row, w_row, acc);
 
     const int mw = wave / T::WN * T::WTM;
     if constexpr (SWIGLU) {
@@ -198,7 +197,13 @@ hipError_t launch_t(GroupedDev p, hipStream_t stream) {
     p.tiles_n = (p.cols + COLS - 1) / COLS;
     p.max_tiles_m = (int)group_tiles(p.rows, p.groups, T::BM);
     const int64_t grid = tile_grid((int64_t)p.max_tiles_m * p.tiles_n);
-    hipLaunchKernelGGL((k_mx_grouped<T, OT, SWIGLU>), dim3((unsigned)grid), dim3(T::NT), 0, stream, p);
+    if constexpr (T::A_MX && !(T::BM == 128 && T::BN == 128)) {  // (which no streamed product picks)
+        if (p.stream) {
+            hipLaunchKernelGGL((k_mx_grouped<T, OT, SWIGLU, true>), dim3((unsigned)grid), dim3(T::NT), 0, stream, p);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((k_mx_grouped<T, OT, SWIGLU, false>), dim3((unsigned)grid), dim3(T::NT), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -256,6 +261,7 @@ hipError_t launch_mx_grouped(const MxGroupedArgs &a, int num_cus, hipStream_t st
     p.cscales = a.c_q ? a.c_q->scales : nullptr;
     p.ldc = a.c_q ? p.cols : a.ldc;
     p.vec_c = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc * (a.c_dtype == NVFP4_F32 ? 4 : 2) % 16 == 0;
+    p.stream = a_mx && grouped_streams(a.rows, a.groups, p.N, p.K);
     const int cfg = plan_grouped(a.rows, a.groups, p.N, p.K, a_mx, num_cus);
     if (cfg < 0) return hipErrorInvalidConfiguration;
     return a_mx ? launch_out<true>(p, a, cfg, stream) : launch_out<false>(p, a, cfg, stream);

@@ -149,4 +149,18 @@ inline int plan_grouped(int64_t rows, int64_t groups, int64_t N, int64_t K, bool
     return best;
 }
 
+// Whether a grouped product with MXFP4 activations loads W past the caches.  Streamed, W does not drive out the lines of scale
+// bytes, of which eight windows share one; but a row tile then finds nothing of W that another has loaded.  So where the L2s do
+// not hold W anyway, or where most groups are one row tile.  Microseconds streamed and not (rows, groups, N x K; the pick marked):
+//   768, 1, 3000 x 4096      22.7, 17.1 *     32768, 1, 4096 x 2048    197, 184 *      24000, 16, 700 x 1024   35.3, 33.1 *
+//   1500, 4, 3000 x 4096     25.7, 23.3 *     16384, 8, 4096 x 2048    114, 111 *      6000, 2, 4096 x 8192    128, 123 *
+//   256, 8, 4096 x 2048      14.0 *, 14.8     768, 64, 3000 x 4096     75.1 *, 79.6    200, 128, 4096 x 8192   213 *, 240
+//   4096, 64, 4096 x 2048    86.4 *, 91.0     32768, 64, 4096 x 2048   252 *, 262      24000, 128, 1536 x 2048 96.2 *, 99.6
+// It does not fit everywhere: 1500, 32, 3000 x 4096 59.8 *, 54.7; 1500, 16, the same 50.6 *, 47.3; 256, 1, 4096 x 2048 8.2, 8.8 *;
+// 200, 2, 4096 x 8192 22.9, 24.0 *.
+// (W4A16 never streams: its steps take a quarter of a line, and gate and up of 96 tokens took 166 instead of 100.)
+inline bool grouped_streams(int64_t rows, int64_t groups, int64_t N, int64_t K) {
+    return rows <= 32 * groups || groups * N * (K / 2) >= (int64_t)48 << 20;
+}
+
 }  // namespace nvfp4

@@ -4,8 +4,9 @@ import pytest
 import torch
 
 import mx_ref
+import mx_stream_shapes
 from gpu_util import DEV
-from test_mx_groups_gpu import check, check_sort, expected, experts, sum_bound
+from test_mx_groups_gpu import check, check_sort, expected, experts, offsets_of, operands, sum_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +128,20 @@ def test_layer_against_float64(nv, t, e, k, h, i, quantize_acts, logits_dt):
         want += p * z
         err += p * (dz + 2.0 ** -17 * (z.abs() + dz))  # the weight, and k products and sums
     check(y, want, err, torch.float32)
+
+
+@pytest.mark.parametrize("shape, tile", mx_stream_shapes.STREAMED)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_w_past_the_caches(nv, shape, tile, swiglu):
+    sizes, n, k = shape
+    print(sizes[:4], n, k, tile, swiglu, flush=True)
+    total = sum(sizes)
+    a, ad, w, wd = operands(nv, n, total // 2 + 1, len(sizes) * n, k, "mx")
+    rows = torch.randint(-1, total // 2 + 2, (total,), generator=gen(1), device=DEV).to(torch.int32)  # some outside A
+    want, err = expected(ad, wd, sizes, rows, swiglu)
+    for dt in (torch.float32, torch.bfloat16):
+        check(nv.mx_grouped_gemm(a, w, offsets_of(sizes), rows=rows, swiglu=swiglu, dtype=dt), want, err, dt)
+    if swiglu and want.shape[1] % 32 == 0:
+        q = nv.mx_grouped_gemm(a, w, offsets_of(sizes), rows=rows, swiglu=True, out=nv.MXFP4Tensor.empty(total, want.shape[1], DEV))
+        same = nv.mx_quantize(nv.mx_grouped_gemm(a, w, offsets_of(sizes), rows=rows, swiglu=True))
+        assert torch.equal(q.codes, same.codes) and torch.equal(q.scales, same.scales)

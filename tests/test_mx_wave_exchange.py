@@ -75,7 +75,7 @@ def compiled(tmp_path_factory):
 
 
 # Sums on their way to C: each wave writes rows of its own part of LDS, a value a lane, and reads them back as whole pieces.
-@pytest.mark.parametrize("source, name, many", [("mx_grouped.hip", "k_mx_grouped", 45), ("mx_gemm.hip", "k_mx_tile", 30),
+@pytest.mark.parametrize("source, name, many", [("mx_grouped.hip", "k_mx_grouped", 60), ("mx_gemm.hip", "k_mx_tile", 30),
                                                 ("mx_gemm.hip", "k_adapter_tile", 30)])
 def test_sums_on_their_way_to_c(compiled, source, name, many):
     found = kernels(compiled(source), name)
