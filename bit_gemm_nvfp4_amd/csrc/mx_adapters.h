@@ -13,6 +13,8 @@
 //     16 bytes from 32 rows an instruction, the branch of 4096 x 4096, rank 64, took 20 us.)  T of the
 //     others' rows is zero then.  4096 x 4096 x 4096 W4A4, rank 64, 7 requests: 54 us with the product, which takes 38 us alone
 //     (44 with rows in another order and no adapter).
+//     The order is the sort's, of at most 511 adapters.  With more the rows stay as they come, and a tile of mixed rows has many:
+//     the same sizes at random over 511 adapters 343 us, over 512 1524 us; 7 requests of 512 side by side 71 us (80 of 511).
 #pragma once
 
 #include "mx_tile.h"

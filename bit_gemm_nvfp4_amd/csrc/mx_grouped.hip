@@ -11,7 +11,8 @@
 // makes it from the fp32 value), without its halves ever being in memory.
 //
 // What bounds it, kernel times:
-//   a few rows per group: streaming the groups' W.  256 rows, 64 groups, 4096 x 1536, W4A16 50 us, 4.3 TB/s of W.
+//   a few rows per group: streaming the groups' W.  256 rows, 64 groups of which 50 have rows, 4096 x 1536, W4A16 50 us; of W
+//     167 MB are needed, 3.3 TB/s, and 176 MB fetched.
 //   prompts, W4A16: matrix instructions and the W expansion between them.  4096 rows, 16 groups, gate and up of 4096 x
 //     4096 157 us, 0.87 PFLOP/s: about 2.4 rounds of tiles, of which the last is not full, and last tiles of a group that
 //     are not.
@@ -42,7 +43,7 @@ struct GroupedDev {
     int64_t ldc;
     uint8_t *cscales;
     int tiles_n, max_tiles_m, vec_c;
-    bool stream;   // W passes the caches by (MXFP4 A)
+    bool stream_w;  // W passes the caches by (MXFP4 A)
 };
 
 // Rows lo .. hi - 1 of group g, whatever the offsets hold: within the rows of C.
@@ -198,7 +199,7 @@ hipError_t launch_t(GroupedDev p, hipStream_t stream) {
     p.max_tiles_m = (int)group_tiles(p.rows, p.groups, T::BM);
     const int64_t grid = tile_grid((int64_t)p.max_tiles_m * p.tiles_n);
     if constexpr (T::A_MX && !(T::BM == 128 && T::BN == 128)) {  // (which no streamed product picks)
-        if (p.stream) {
+        if (p.stream_w) {
             hipLaunchKernelGGL((k_mx_grouped<T, OT, SWIGLU, true>), dim3((unsigned)grid), dim3(T::NT), 0, stream, p);
             return hipGetLastError();
         }
@@ -261,7 +262,7 @@ hipError_t launch_mx_grouped(const MxGroupedArgs &a, int num_cus, hipStream_t st
     p.cscales = a.c_q ? a.c_q->scales : nullptr;
     p.ldc = a.c_q ? p.cols : a.ldc;
     p.vec_c = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc * (a.c_dtype == NVFP4_F32 ? 4 : 2) % 16 == 0;
-    p.stream = a_mx && grouped_streams(a.rows, a.groups, p.N, p.K);
+    p.stream_w = a_mx && grouped_streams(a.rows, a.groups, p.N, p.K);
     const int cfg = plan_grouped(a.rows, a.groups, p.N, p.K, a_mx, num_cus);
     if (cfg < 0) return hipErrorInvalidConfiguration;
     return a_mx ? launch_out<true>(p, a, cfg, stream) : launch_out<false>(p, a, cfg, stream);

@@ -10,8 +10,12 @@
 //   depends on timing.  Few rows are
 //   done by one workgroup in one launch.
 // k_mx_combine: y[t] = sum_j w[t][j] z[places[t][j]] in fp32, in the order of j.  Bound by reading z: 4096 x 4096, four rows
-//   each, bf16 28 us, 5.4 TB/s.
-// The router is bound by latency: 16 rows 6.8 us, 4096 x 64 6.4 + 7.2 us (two launches), 16384 x 128, top 8 7.8 + 8.1 us.
+// each, bf16 27 us: z's 134 MB at 4.9 TB/s, with y's 34 MB 6.2 TB/s (part of z is in the caches).
+// The router is bound by latency: 16 rows 6.8 us, 4096 x 64 6.4 + 7.2 us (two launches), 16384 x 128, top 8 7.8 + 8.1 us.  A row has
+// registers for 64, 128, 256 or 512 entries, so just above one of them it costs as much as at the next: 16384 rows, top 8, of 64,
+// 65, 128, 129, 256 and 257 entries 12.5, 15.3, 15.8, 20.9, 22.0 and 33.1 us.
+// The sort alone, eight choices of 64 groups: 64 rows 4.8 us, 512 9.6 (one workgroup), 513 13.9 (two launches); 2^20 rows of two
+// choices, 128 groups 34 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -330,7 +330,8 @@ def mx_grouped_gemm(a: torch.Tensor | MXFP4Tensor, w: MXFP4Tensor, offsets: torc
     a: MXFP4Tensor (W4A4) or bf16 [R, K] (W4A16); rows: int32, the row of A of each row of C (all of A's, in order,
     without it; one outside A counts as zeros); w [groups * N, K], groups stacked (swiglu: N / 2 gate rows, then N / 2 up
     rows, per group).  Returns C [len(rows) or R, N or N / 2], fp32 or bf16; with swiglu `out` may be an MXFP4Tensor, which
-    is quantized from the fp32 values.  Rows outside every group are left as they are in `out`."""
+    is quantized from the fp32 values.  Rows outside every group (those behind the last one, where
+    a router has masked experts) are left as they are in `out`; without `out` they hold anything, NaN included."""
     assert isinstance(w, MXFP4Tensor), "w: an MXFP4Tensor is required"
     wr, k = w.shape
     dev = w.codes.device
@@ -394,8 +395,11 @@ def mx_experts(x: torch.Tensor, logits: torch.Tensor, w_gate_up: MXFP4Tensor, w_
                routing: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The mixture-of-experts layer of mx_moe for any number of tokens (a prompt, a large batch): router, grouped
     products and weighted sum.  With quantize_acts x and silu(gate) * up go through MXFP4 (W4A4), else through bf16 (W4A16);
-    what an expert gives a token is rounded to y's type before the weighted fp32 sum.  mx_moe keeps more bits and is
-    faster for few tokens.  Arguments, layouts and returns as for mx_moe (a row with NaN or +inf has NaN weights)."""
+    what an expert gives a token is rounded to y's type before the weighted fp32 sum.
+
+    In place of mx_moe: quantize_acts is True unless given, so that activations have four bits, which mx_moe's never have;
+    quantize_acts=False keeps them in bf16, and mx_moe, for up to 64 tokens, in fp32's bits.  mx_moe is the faster one up to about
+    ten tokens.  Else arguments, layouts and returns are mx_moe's (a row with NaN or +inf has NaN weights)."""
     dev = x.device
     assert x.dtype is torch.bfloat16, f"x: bf16, not {x.dtype}"
     assert logits.dtype in (torch.float32, torch.bfloat16), f"logits: fp32 or bf16, not {logits.dtype}"
@@ -443,7 +447,8 @@ def mx_gemm_adapters(a: torch.Tensor, w: MXFP4Tensor, down: torch.Tensor, up: to
     down[i]^T) . up[i]^T with i = index[m] (int32 [M], any order; outside 0 .. adapters - 1: no adapter).
 
     a: bf16 [M, K]; a_q: its MXFP4 form, for a W4A4 product (the branch takes `a`); w [N, K]; down [adapters, rank, K] and up
-    [adapters, N, rank] bf16, dense, rank a multiple of 8 up to 256; scales fp32 [adapters].  C fp32 or bf16, rounded once."""
+    [adapters, N, rank] bf16, dense, rank a multiple of 8 up to 256; scales fp32 [adapters].  C fp32 or bf16, rounded once.  From 512 adapters
+    on rows of different adapters in turn are several times slower than side by side (include/mxfp4.h)."""
     assert isinstance(w, MXFP4Tensor), "w: an MXFP4Tensor is required"
     n, k = w.shape
     dev = w.codes.device

@@ -165,7 +165,8 @@ nvfp4_status mxfp4_group_rows(const int32_t *ids, int64_t tokens, int per_token,
  *   c        [rows x N] (swiglu: N / 2) fp32 or bf16, row stride ldc; or c_q, an MXFP4 tensor of that shape (swiglu
  *            only), as mxfp4_quantize makes it from the fp32 values.  Exactly one.
  * Sums and silu are fp32, rounded once to C.  A group may be empty; rows of C outside every group are left as they are.
- * W4A16 and W4A4 as for mxfp4_gemm.  No workspace.
+ * W4A16 and W4A4 as for mxfp4_gemm.  No workspace.  K is not split over workgroups: a few rows in a few groups are slower than as
+ * products of their own (mxfp4_gemm).
  * Errors: NVFP4_ERR_SHAPE for rows or a_rows > MXFP4_GROUP_MAX_ROWS, groups < 1 or > MXFP4_MAX_GROUPS, K == 0, K or
  * lda above 2^20, w->rows not a multiple of groups (with swiglu: of 2 groups), N above 2^24, with a map a_rows rows of A
  * of 2^31 bytes or more, with swiglu N / 2 rows of W of 2^30 bytes or more, more output tiles than one launch holds, or
@@ -224,6 +225,10 @@ enum { MXFP4_MAX_ADAPTERS = 1 << 16, MXFP4_MAX_RANK = 256 };
  * Sums are fp32 (A . V^T too, which passes on with fp32's 24 bits), and C is rounded once.  What an adapter holds reaches
  * the rows that name it and no others.  A NaN or infinity in V or U gives NaN or infinity in rows that name that adapter.
  * index, down, up and scales are read on the device.
+ * Speed: with more than 64 rows and 2 to 511 adapters the rows are taken in the order of their adapters, so that a tile of C has
+ * few.  With 512 adapters or more (however many the rows name), and where M * max(2 lda, K) reaches 2^31, they are taken as they
+ * come, which costs as much where an adapter's rows lie side by side and several times as much where they are mixed: group them
+ * before the call then, or pass the batch's own adapters alone.
  * workspace (16-byte aligned; none without adapters): with mxfp4_adapters_workspace_size(...) bytes a long K may be split as
  * in mxfp4_gemm; what that size is for K = 32 is needed in any case (NVFP4_ERR_WORKSPACE for less).  quantized_acts: whether
  * a_q is given.  M <= MXFP4_GROUP_MAX_ROWS, lda <= 2^21; else limits and errors as for mxfp4_gemm.
