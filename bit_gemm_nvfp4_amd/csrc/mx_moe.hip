@@ -397,6 +397,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeDev a) {
                 s += acc[t];
                 *dst = s;
             }
+            wave_exchange();  // other lanes may hold the token in the next unit
         }
     };
     constexpr int STEP = kDownWaves * RT;

@@ -85,3 +85,13 @@ def test_sums_on_their_way_to_c(compiled, source, name, many):
         assert sum(value(*s) for body, _ in f.blocks.values() for s in f.steps(body)) >= 16, kernel
         assert not f.unordered(value, piece, same_block=True), kernel
         assert not f.unordered(piece, value, same_block=True), kernel
+
+
+def test_sums_of_a_token_in_the_layer_for_few_tokens(compiled):
+    # a token's sums are added to by whichever lanes hold it in the expert at hand
+    found = kernels(compiled("mx_moe.hip"), "k_moe_down")
+    assert len(found) == 4
+    for kernel, f in found.items():
+        store, load = lambda kind, ty, off: (kind, ty) == ("S", "<4 x float>"), lambda kind, ty, off: (kind, ty) == ("L", "<4 x float>")
+        assert any(store(*s) for body, _ in f.blocks.values() for s in f.steps(body)), kernel
+        assert not f.unordered(store, load, same_block=False), kernel
